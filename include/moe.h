@@ -423,6 +423,92 @@ int moe_weight_grads(const moe_shape* shape, const void* x, const int32_t* sorte
 int moe_bias_grad(const moe_shape* shape, const float* dz, float* dbias, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The two ends of a training step around the layer: the pre-norm that makes its
+ * input, and the update made of its weight gradients.  Sizes are arguments of
+ * their own (a norm runs over any width, an update over any matrix); pointers,
+ * streams, errors and empty inputs as above.  dtype is a moe_dtype.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+
+/* Pre-norm, with the residual addition before it ("Laguna-M.1-base",
+ * Normalisation: RMS norm in fp32; layer norm beside it), per row:
+ *   s = x + residual, rounded to elem (s = x without a residual)
+ *   mean = sum s / cols (MOE_NORM_LAYER; 0 for MOE_NORM_RMS)
+ *   rstd = 1 / sqrt(sum (s - mean)^2 / cols + eps)
+ *   y = (s - mean) * rstd * gamma + beta
+ *   x, residual  [rows, cols] elem; residual may be NULL
+ *   gamma, beta  [cols] fp32; NULL = ones, zeros
+ *   eps          > 0
+ *   sum          [rows, cols] elem out: s; needed with a residual, NULL without
+ *   y            [rows, cols] elem out
+ *   mean, rstd   [rows] fp32 out, what moe_norm_backward needs; either may be
+ *                NULL; mean is not written for MOE_NORM_RMS
+ * sum or y may be x or residual itself (not each other); no other overlap.
+ * cols <= 16384 (else MOE_ERR_UNSUPPORTED), any width from 1; rows >= 0.  The
+ * statistics are fp32, the variance summed around the mean. */
+int moe_norm_forward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, const void* x,
+                     const void* residual, const float* gamma, const float* beta, float eps, void* sum,
+                     void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace moe_norm_backward needs for its column sums (0 for sizes
+ * it rejects, and for rows == 0). */
+size_t moe_norm_workspace_bytes(int64_t rows, int32_t cols);
+
+/* Backward of moe_norm_forward: with h = (x - mean) rstd, t = dy gamma, per row
+ *   dx = rstd (t - h sum(t h) / cols - sum t / cols [MOE_NORM_LAYER]) + dsum
+ * and dgamma = sum over rows of dy h, dbeta = sum over rows of dy.
+ *   x          [rows, cols] elem: the normalised input (the forward's sum where
+ *              it had a residual)
+ *   mean, rstd from the forward (mean may be NULL for MOE_NORM_RMS)
+ *   gamma      as in the forward
+ *   dsum       [rows, cols] elem or NULL: the gradient that arrives at s on its
+ *              other way (the residual stream); dx is then the gradient of both
+ *              x and residual
+ *   dx         [rows, cols] elem out; may be dy, x or dsum itself
+ *   dgamma, dbeta [cols] fp32 out; either may be NULL
+ *   workspace  >= moe_norm_workspace_bytes bytes (not needed without dgamma and
+ *              dbeta)
+ * The sums over rows run in a fixed order: the results are bit-reproducible.
+ * rows == 0 writes zeros to dgamma and dbeta. */
+int moe_norm_backward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, const void* dy,
+                      const void* x, const float* gamma, const float* mean, const float* rstd,
+                      const void* dsum, void* dx, float* dgamma, float* dbeta, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace moe_orthogonalize needs (0 for sizes it rejects, and for
+ * empty ones): about 8 to 18 bytes an element of g, more for square and small
+ * matrices. */
+size_t moe_orthogonalize_workspace_bytes(int64_t count, int32_t rows, int32_t cols);
+
+/* Orthogonalised update of `count` weight matrices, the direction of the Muon
+ * optimiser ("Laguna M.1/XS.2 Technical Report", Key claims: training with
+ * Muon, Newton-Schulz iterations per parameter), per matrix:
+ *   without momentum  u = g
+ *   with momentum M   M <- mu M + g;  u = g + mu M (nesterov != 0) or M
+ *   x = u / (|u|_F + eps)
+ *   steps times       x <- (a I + b R + c R^2) x,  R = x x^T (on the shorter side),
+ *                     (a, b, c) = (3.4445, -4.7750, 2.0315)
+ *   out = scale * x
+ *   g         [count, rows, cols] elem (MOE_BF16 as moe_weight_grads writes
+ *             dw_gate_up and dw_down, or MOE_F32 as dw_router)
+ *   momentum  [count, rows, cols] fp32, updated in place, or NULL
+ *   mu        in [0, 1) (read only with a momentum)
+ *   steps     1 .. 16; eps >= 0; scale finite
+ *   out       [count, rows, cols] bf16 for either dtype; may be g itself when g
+ *             is bf16; no other overlap
+ *   workspace >= moe_orthogonalize_workspace_bytes bytes
+ * A zero matrix gives zeros; an infinity or a NaN in u makes that matrix's
+ * output NaN and touches no other.  Products run on fp16 operands with fp32
+ * accumulation, held finer where the result needs it (error against 64 bits
+ * about the rounding of the bf16 output).
+ * rows * cols < 2^30, count <= 65535, count * rows * cols < 2^36 (else
+ * MOE_ERR_UNSUPPORTED). */
+int moe_orthogonalize(int64_t count, int32_t rows, int32_t cols, int32_t dtype, const void* g,
+                      float* momentum, float mu, int32_t nesterov, int32_t steps, float eps, float scale,
+                      void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16 = 0, 1
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
 
 # the entry points include/moe.h declares
 EXPORTS = ("moe_version", "moe_status_string", "moe_last_error", "moe_workspace_bytes",
@@ -31,7 +32,9 @@ EXPORTS = ("moe_version", "moe_status_string", "moe_last_error", "moe_workspace_
            "moe_route_masked", "moe_train_workspace_bytes", "moe_packed_transposed_bytes",
            "moe_pack_weights_transposed", "moe_load_stats", "moe_grouped_gate_up_train",
            "moe_combine_backward", "moe_grouped_backward_h", "moe_grouped_backward_x",
-           "moe_weight_grads", "moe_bias_grad", "moe_shared_ffn", "moe_permute_static")
+           "moe_weight_grads", "moe_bias_grad", "moe_shared_ffn", "moe_permute_static",
+           "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward",
+           "moe_orthogonalize_workspace_bytes", "moe_orthogonalize")
 
 
 class moe_shape(ctypes.Structure):
@@ -123,6 +126,18 @@ def lib() -> ctypes.CDLL:
         L.moe_weight_grads.argtypes = [_SP] + [_P] * 15
         L.moe_bias_grad.restype = ctypes.c_int
         L.moe_bias_grad.argtypes = [_SP, _P, _P, _P, ctypes.c_size_t, _P]
+        # pre-norm and orthogonalised update
+        i32, i64, f32, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        L.moe_norm_forward.restype = ctypes.c_int
+        L.moe_norm_forward.argtypes = [i32, i64, i32, i32, _P, _P, _P, _P, f32, _P, _P, _P, _P, _P]
+        L.moe_norm_workspace_bytes.restype = size
+        L.moe_norm_workspace_bytes.argtypes = [i64, i32]
+        L.moe_norm_backward.restype = ctypes.c_int
+        L.moe_norm_backward.argtypes = [i32, i64, i32, i32] + [_P] * 10 + [size, _P]
+        L.moe_orthogonalize_workspace_bytes.restype = size
+        L.moe_orthogonalize_workspace_bytes.argtypes = [i64, i32, i32]
+        L.moe_orthogonalize.restype = ctypes.c_int
+        L.moe_orthogonalize.argtypes = [i64, i32, i32, i32, _P, _P, f32, i32, i32, f32, f32, _P, _P, size, _P]
         _lib = L
     return _lib
 
@@ -610,3 +625,83 @@ def train_backward(s: MoEShape, x: torch.Tensor, dout: torch.Tensor, w: TrainWei
                      b.dw_gate_up, b.dw_down, b.dws_gate_up, b.dws_down, b.dw_router, stream)
     moe_bias_grad(c, b.dz, b.dbias, b.train_ws, stream)
     return b.dx
+
+
+# ---------------------------------------------------------------------------
+# the ends of a training step: pre-norm and orthogonalised update
+# ---------------------------------------------------------------------------
+
+def _elem(t: torch.Tensor, what: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return MOE_BF16
+    if t.dtype == torch.float32:
+        return MOE_F32
+    raise ValueError(f"{what} is {t.dtype}: float32 or bfloat16 is wanted")
+
+
+def _expect(t: Optional[torch.Tensor], shape, dtype, device, what: str) -> None:
+    """These entry points take their sizes from a tensor, so the others' are checked here."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}: "
+                         f"{tuple(shape)} {dtype} on {device} is wanted")
+
+
+def _stream_of(stream, t: torch.Tensor) -> int:
+    """The given stream, or the current one of the tensors' device, which has to be the current device
+    (the library launches on the current device)."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device} while cuda:{torch.cuda.current_device()} is current")
+    return _stream(stream)
+
+
+def moe_norm_workspace_bytes(rows, cols) -> int:
+    return int(lib().moe_norm_workspace_bytes(int(rows), int(cols)))
+
+
+def moe_norm_forward(kind, x, residual, gamma, beta, eps, sum, y, mean, rstd, stream=None):
+    """Pre-norm of the rows of x [rows, cols] (+ residual)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    for t, what in ((residual, "residual"), (sum, "sum"), (y, "y")):
+        _expect(t, (rows, cols), x.dtype, x.device, what)
+    for t, n, what in ((gamma, cols, "gamma"), (beta, cols, "beta"), (mean, rows, "mean"), (rstd, rows, "rstd")):
+        _expect(t, (n,), torch.float32, x.device, what)
+    _check(lib().moe_norm_forward(int(kind), rows, cols, _elem(x, "x"), _ptr(x), _ptr(residual), _ptr(gamma),
+                                  _ptr(beta), float(eps), _ptr(sum), _ptr(y), _ptr(mean), _ptr(rstd),
+                                  _stream_of(stream, x)), "moe_norm_forward")
+
+
+def moe_norm_backward(kind, dy, x, gamma, mean, rstd, dsum, dx, dgamma, dbeta, workspace, stream=None):
+    """Gradients of the pre-norm; x is what was normalised (the forward's sum where it had a residual)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, cols]")
+    rows, cols = x.shape
+    for t, what in ((dy, "dy"), (dsum, "dsum"), (dx, "dx")):
+        _expect(t, (rows, cols), x.dtype, x.device, what)
+    for t, n, what in ((gamma, cols, "gamma"), (mean, rows, "mean"), (rstd, rows, "rstd"), (dgamma, cols, "dgamma"),
+                       (dbeta, cols, "dbeta")):
+        _expect(t, (n,), torch.float32, x.device, what)
+    _check(lib().moe_norm_backward(int(kind), rows, cols, _elem(x, "x"), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean),
+                                   _ptr(rstd), _ptr(dsum), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+                                   _nbytes(workspace), _stream_of(stream, x)), "moe_norm_backward")
+
+
+def moe_orthogonalize_workspace_bytes(count, rows, cols) -> int:
+    return int(lib().moe_orthogonalize_workspace_bytes(int(count), int(rows), int(cols)))
+
+
+def moe_orthogonalize(g, momentum, mu, nesterov, steps, eps, scale, out, workspace, stream=None):
+    """Orthogonalised update of g [rows, cols] or [count, rows, cols] into out (bf16), through the momentum
+    (fp32, updated in place) where there is one."""
+    if g.dim() not in (2, 3):
+        raise ValueError("g must be [rows, cols] or [count, rows, cols]")
+    count = g.shape[0] if g.dim() == 3 else 1
+    rows, cols = g.shape[-2:]
+    _expect(momentum, g.shape, torch.float32, g.device, "momentum")
+    _expect(out, g.shape, torch.bfloat16, g.device, "out")
+    _check(lib().moe_orthogonalize(count, rows, cols, _elem(g, "g"), _ptr(g), _ptr(momentum), float(mu),
+                                   int(bool(nesterov)), int(steps), float(eps), float(scale), _ptr(out),
+                                   _ptr(workspace), _nbytes(workspace), _stream_of(stream, g)), "moe_orthogonalize")

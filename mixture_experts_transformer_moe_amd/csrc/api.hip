@@ -607,4 +607,128 @@ int moe_bias_grad(const moe_shape* shape, const float* dz, float* dbias, void* w
   return launched(moe::launch_colsum(*shape, dz, dbias, workspace, as_stream(stream)));
 }
 
+// ------------------------------------------------------------- pre-norm, update
+
+namespace {
+
+int check_norm(int32_t kind, int64_t rows, int32_t cols, int32_t dtype) {
+  if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS)
+    return fail(MOE_ERR_INVALID_ARG, "kind %d is neither MOE_NORM_LAYER nor MOE_NORM_RMS", kind);
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "dtype %d is neither MOE_F32 nor MOE_BF16", dtype);
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %lld < 0", static_cast<long long>(rows));
+  if (cols < 1) return fail(MOE_ERR_INVALID_ARG, "cols = %d < 1", cols);
+  if (cols > moe::kNormMaxCols) return fail(MOE_ERR_UNSUPPORTED, "cols = %d > %d", cols, moe::kNormMaxCols);
+  if (rows >= (int64_t{1} << 40)) return fail(MOE_ERR_UNSUPPORTED, "rows = %lld >= 2^40", static_cast<long long>(rows));
+  return MOE_OK;
+}
+
+int check_orth(int64_t count, int32_t rows, int32_t cols) {
+  if (count < 0 || rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "negative count or size");
+  const int64_t elems = static_cast<int64_t>(rows) * cols;
+  if (elems >= (int64_t{1} << 30)) return fail(MOE_ERR_UNSUPPORTED, "rows * cols = %lld >= 2^30", static_cast<long long>(elems));
+  if (count > 65535) return fail(MOE_ERR_UNSUPPORTED, "count = %lld > 65535", static_cast<long long>(count));
+  if (count * elems >= (int64_t{1} << 36)) return fail(MOE_ERR_UNSUPPORTED, "count * rows * cols >= 2^36");
+  return MOE_OK;
+}
+
+// do [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && p < q + nb && q < p + na;
+}
+
+}  // namespace
+
+int moe_norm_forward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, const void* x,
+                     const void* residual, const float* gamma, const float* beta, float eps, void* sum,
+                     void* y, float* mean, float* rstd, void* stream) {
+  if (int r = check_norm(kind, rows, cols, dtype)) return r;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be positive and finite");
+  if ((residual != nullptr) != (sum != nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "sum goes with a residual, and a residual with sum");
+  if (rows == 0) return ok();
+  NEED_PTR(x);
+  OPT_PTR(residual);
+  OPT_PTR(gamma);
+  OPT_PTR(beta);
+  OPT_PTR(sum);
+  NEED_PTR(y);
+  OPT_PTR(mean);
+  OPT_PTR(rstd);
+  const bool bf16 = dtype == MOE_BF16, layer = kind == MOE_NORM_LAYER;
+  const size_t bytes = static_cast<size_t>(rows) * cols * (bf16 ? 2 : 4);
+  if (overlap(sum, bytes, y, bytes)) return fail(MOE_ERR_INVALID_ARG, "sum and y overlap");
+  for (const void* out : {static_cast<const void*>(sum), static_cast<const void*>(y)})
+    for (const void* in : {x, residual})
+      if (out != in && overlap(out, bytes, in, bytes))
+        return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input without being it");
+  return launched(moe::launch_norm_forward(layer, rows, cols, bf16, x, residual, gamma, beta, eps, sum, y,
+                                           layer ? mean : nullptr, rstd, as_stream(stream)));
+}
+
+size_t moe_norm_workspace_bytes(int64_t rows, int32_t cols) {
+  if (check_norm(MOE_NORM_RMS, rows, cols, MOE_BF16) != MOE_OK || rows == 0) return 0;
+  return moe::norm_workspace_bytes(rows, cols);
+}
+
+int moe_norm_backward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, const void* dy,
+                      const void* x, const float* gamma, const float* mean, const float* rstd,
+                      const void* dsum, void* dx, float* dgamma, float* dbeta, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (int r = check_norm(kind, rows, cols, dtype)) return r;
+  OPT_PTR(dgamma);
+  OPT_PTR(dbeta);
+  const bool bf16 = dtype == MOE_BF16, layer = kind == MOE_NORM_LAYER;
+  if (rows > 0) {
+    NEED_PTR(dy);
+    NEED_PTR(x);
+    OPT_PTR(gamma);
+    if (layer) NEED_PTR(mean);
+    NEED_PTR(rstd);
+    OPT_PTR(dsum);
+    NEED_PTR(dx);
+    const size_t bytes = static_cast<size_t>(rows) * cols * (bf16 ? 2 : 4);
+    for (const void* in : {dy, x, dsum})
+      if (dx != in && overlap(dx, bytes, in, bytes))
+        return fail(MOE_ERR_INVALID_ARG, "dx overlaps an input without being it");
+    if (dgamma != nullptr || dbeta != nullptr) {
+      if (int r = check_workspace(workspace, workspace_bytes, moe::norm_workspace_bytes(rows, cols))) return r;
+    }
+  }
+  return launched(moe::launch_norm_backward(layer, rows, cols, bf16, dy, x, gamma, mean, rstd, dsum, dx, dgamma,
+                                            dbeta, workspace, as_stream(stream)));
+}
+
+size_t moe_orthogonalize_workspace_bytes(int64_t count, int32_t rows, int32_t cols) {
+  if (check_orth(count, rows, cols) != MOE_OK || count == 0 || rows == 0 || cols == 0) return 0;
+  return moe::orth_workspace_bytes(count, rows, cols);
+}
+
+int moe_orthogonalize(int64_t count, int32_t rows, int32_t cols, int32_t dtype, const void* g,
+                      float* momentum, float mu, int32_t nesterov, int32_t steps, float eps, float scale,
+                      void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int r = check_orth(count, rows, cols)) return r;
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "dtype %d is neither MOE_F32 nor MOE_BF16", dtype);
+  if (steps < 1 || steps > 16) return fail(MOE_ERR_INVALID_ARG, "steps = %d outside 1..16", steps);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (!std::isfinite(scale)) return fail(MOE_ERR_INVALID_ARG, "scale is not finite");
+  if (momentum != nullptr && !(mu >= 0.0f && mu < 1.0f)) return fail(MOE_ERR_INVALID_ARG, "mu outside [0, 1)");
+  if (count == 0 || rows == 0 || cols == 0) return ok();
+  NEED_PTR(g);
+  OPT_PTR(momentum);
+  NEED_PTR(out);
+  const size_t n = static_cast<size_t>(count) * rows * cols;
+  const bool bf16 = dtype == MOE_BF16;
+  const size_t need = moe::orth_workspace_bytes(count, rows, cols);
+  if (int r = check_workspace(workspace, workspace_bytes, need)) return r;
+  if ((!(bf16 && out == g) && overlap(out, 2 * n, g, n * (bf16 ? 2 : 4))) || overlap(out, 2 * n, momentum, 4 * n) ||
+      overlap(g, n * (bf16 ? 2 : 4), momentum, 4 * n) || overlap(workspace, need, out, 2 * n) ||
+      overlap(workspace, need, g, n * (bf16 ? 2 : 4)) || overlap(workspace, need, momentum, 4 * n))
+    return fail(MOE_ERR_INVALID_ARG, "g, momentum, out and workspace overlap");
+  return launched(moe::launch_orthogonalize(count, rows, cols, bf16, g, momentum, mu, nesterov != 0, steps, eps,
+                                            scale, static_cast<moe::bf16_t*>(out), workspace, as_stream(stream)));
+}
+
 }  // extern "C"

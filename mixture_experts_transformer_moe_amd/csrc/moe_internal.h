@@ -136,4 +136,21 @@ hipError_t launch_wgrad(const moe_shape& s, const bf16_t* x, const int32_t* sort
                         const bf16_t* dout, const bf16_t* dz16, const int32_t* offsets, bf16_t* dwgu,
                         bf16_t* dwd, bf16_t* dwsgu, bf16_t* dwsd, float* dwr, hipStream_t st);
 
+// ------------------------------------------------------- pre-norm (norm.hip)
+constexpr int kNormMaxCols = 16384;
+size_t norm_workspace_bytes(int64_t rows, int cols);
+hipError_t launch_norm_forward(bool layer, int64_t rows, int cols, bool bf16, const void* x,
+                               const void* residual, const float* gamma, const float* beta, float eps,
+                               void* sum, void* y, float* mean, float* rstd, hipStream_t st);
+hipError_t launch_norm_backward(bool layer, int64_t rows, int cols, bool bf16, const void* dy,
+                                const void* x, const float* gamma, const float* mean, const float* rstd,
+                                const void* dsum, void* dx, float* dgamma, float* dbeta, void* workspace,
+                                hipStream_t st);
+
+// -------------------------------------------- orthogonalised update (orth.hip)
+size_t orth_workspace_bytes(int64_t count, int rows, int cols);
+hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, const void* g, float* mom,
+                                float mu, bool nesterov, int steps, float eps, float scale, bf16_t* out,
+                                void* workspace, hipStream_t st);
+
 }  // namespace moe

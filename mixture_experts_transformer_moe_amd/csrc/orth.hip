@@ -1,0 +1,737 @@
+// Orthogonalised update of weight matrices (the direction of the Muon
+// optimiser): Newton-Schulz steps on the matrix cores, batched over experts.
+//
+// Per matrix u (the gradient, or gradient and momentum joined), taken with its
+// short side first (m <= n; a tall matrix is read and written transposed):
+//   x_0 = u / (|u|_F + eps),   x <- (a I + b R + c R^2) x,  R = x x^T,
+// `steps` times, out = scale * x in bf16.
+//
+// Grouping.  The polynomial Q(R) of a step commutes with R, so the next step's
+// Gram matrix is R' = Q R Q, and two steps apply as one product:
+//   x <- Q2(R') Q1(R) x.
+// With symmetric products computing one triangle, the pair costs
+// 3 m^2 n + 5 m^3 flops against 6 m^2 n + 2 m^3 one by one, so the first two
+// steps are taken together where the matrix is wide (n >= 1.5 m).  Later steps
+// are not: R' holds R's small eigenvalues only to its rounding, which does not
+// matter while Q(R) acts on them as a I, but does once the spectrum is flat.
+// Nor are three, nor those of a small matrix (m < 256), whose roundings average
+// over few terms.  Error against 64 bits, relative in norm, of rank-deficient
+// bf16 gradients (the output's own rounding to bf16 is 1.7e-3 of each):
+//                                         1+1+1+1+1  2+1+1+1  3+1+1   3+2
+//   1024 x 2048, rank 128                 1.8e-3     1.8e-3   1.9e-3  2.8e-3
+//   256 x 1024, rank 1 and noise of 1e-3  2.2e-3     2.4e-3   6.3e-3  6.4e-3
+//   32 x 32, rank 16                      2.6e-3     3.4e-3   7.4e-3
+//
+// Numbers.  Products run on fp16 operands with fp32 accumulation: singular
+// directions far below the largest are amplified by a^5 = 485, and bf16's 8
+// bits would add noise of 1% to 30% of the result.  Two parts are kept finer,
+// at no product's cost:
+//   * a symmetric matrix M is stored as its off-diagonal part in fp16 and its
+//     diagonal d in fp32; (M + d)(N + e) = M N + d_i N_ij + M_ij e_j is joined
+//     in fp32 in the epilogue.  The polynomial of a nearly null direction is
+//     a I, whose rounding would otherwise be the largest error;
+//   * x is stored as fp16 hi + lo (22 bits); the products read hi, and the
+//     elementwise part d_i x_ij reads both.
+// Powers of two keep fp16 away from its subnormals: x and R are stored times
+// 2^12 (|x|, |R| < 2), Q and Q2 Q1 times 2^8 (|Q2 Q1| <= a^2 = 12).
+//
+// Layout.  Every matrix of the workspace is a grid of 32 x 16 blocks of 1 KB
+// (row-block major), a block holding the 64 lanes' 16-byte runs of a
+// v_mfma_f32_32x32x16_f16 operand: element (r, c) of a block sits in run
+// (r ^ 4 h ^ 8 o) + 32 h, h = c / 8, o the parity of the block's column.
+//   * a product's stage (32 values of K) is whole kilobytes, loaded straight
+//     into LDS and read as operands at lane order, without a bank conflict;
+//   * x is the transposed operand of the last product of a group (K = its
+//     rows): the transposing LDS read takes it from the same blocks, and the
+//     two XORs put its 8-byte pieces into distinct banks;
+//   * an accumulator block leaves as two whole blocks after one lane-pair
+//     swap; its mirror image (symmetric products) goes through 2 KB of LDS and
+//     the same transposing read.
+// Rows and columns are padded with zeros to multiples of 32 (at least 128):
+// zero rows stay zero, and the padded diagonal of Q meets zero rows of x.
+#include "lds_dma.h"
+
+namespace moe {
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;   // the quintic's coefficients
+constexpr float kSX = 4096.0f;        // stored scale of x and R
+constexpr float kSQ = 256.0f;         // stored scale of Q and products of Qs
+constexpr int kOThreads = 256;        // 4 waves, 2 x 2
+constexpr int kOBK = 32;              // K per stage
+constexpr int kONS = 4;               // stages of the ring
+constexpr int kOXcds = 8;
+constexpr int kMinPad = 128;          // smallest padded side: a tile has at least kONS stages
+
+enum { kGram = 0, kPoly = 1, kMul = 2, kApply = 3, kFinal = 4 };
+
+struct OrthJob {
+  const _Float16* p;        // row operand, [rows / 32][K / 16] blocks
+  const _Float16* q;        // column operand; kApply / kFinal: x hi, [K / 32][n / 16] blocks
+  const _Float16* lo;       // kApply / kFinal: x lo
+  const float* dp;          // diagonals of p and q
+  const float* dq;
+  _Float16* out;            // kFinal: unused
+  _Float16* out_lo;         // kApply: the low part
+  float* dout;
+  float sp, sq, so;         // stored scales of p, q and out
+};
+
+struct OrthArgs {
+  OrthJob job;
+  int count;                // matrices
+  int mb, nb;               // row blocks (32) of the output, column blocks (32)
+  int K;                    // reduction length
+  int64_t p_stride, q_stride, out_stride;   // elements between matrices
+  int d_stride;
+  // kFinal: the caller's matrix
+  bf16_t* user;
+  int rows, cols, tall;     // tall: the caller's matrix is the transpose
+  float scale;
+};
+
+// byte offset of the run of row r, half h (columns 8h..8h+7) in a block whose
+// column block has parity o
+__device__ __forceinline__ int run_off(int r, int h, int o) {
+  return ((r ^ (h << 2) ^ (o << 3)) << 4) + (h << 9);
+}
+
+__device__ __forceinline__ void dma_run(const void* base, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(voff), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v)));
+  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32)));
+  return reinterpret_cast<T*>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// Transposed operand of a 32 x 32 square held as two blocks (columns 0..15 at
+// b, 16..31 at b + 1024): lane l receives rows 16 kk + 8 (l / 32) + 0..7 of
+// column l mod 32.  In a group of 16 lanes ds_read_b64_tr_b16 hands lane 4a + b
+// element b of the 8-byte pieces that lanes a, a + 4, a + 8, a + 12 address:
+// lane j of a group addresses row k0 + j / 4, columns c0 + 4 (j mod 4) .. + 3.
+__device__ __forceinline__ f16x8 tr_run(const unsigned char* b, int kk, int lane) {
+  const int grp = lane >> 4, j = lane & 15;
+  const int row = 16 * kk + 8 * (grp >> 1) + (j >> 2);
+  const int o = grp & 1, h = (j & 3) >> 1;
+  typedef __attribute__((address_space(3))) s16x4 lds_v4;
+  const unsigned char* at = b + 1024 * o + 8 * (j & 1);
+  auto piece = [&](int r) __attribute__((always_inline)) {
+    return (lds_v4*)(reinterpret_cast<__attribute__((address_space(3))) uint16_t*>(lds_addr(at + run_off(r, h, o))));
+  };
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(piece(row));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(piece(row + 4));
+  const s16x4 v[2] = {lo, hi};
+  return __builtin_bit_cast(f16x8, v);
+}
+
+constexpr int wait_vm(int n) { return vmcnt_only(n > 63 ? 63 : n); }
+constexpr int kWaitLds = 15 | (7 << 4) | (0 << 8) | (3 << 14);     // lgkmcnt(0) only
+
+// One product of the iteration.  A tile is TB x TB blocks of 32 (TB = 2 WB),
+// each wave owns WB x WB of them.  The symmetric modes compute the tiles on
+// and below the diagonal and store the mirror image of those below.
+//
+// Schedule: a persistent grid walks the tiles in rounds, each round cut into 8
+// runs of consecutive tiles, one per XCD (workgroup b runs on XCD b mod 8), so
+// that the tiles of one matrix share an L2.  Stages go through a ring of 4; a
+// stage's two MFMA steps read their operands from LDS one step ahead, one
+// barrier a stage sits between them: there every wave has read the stage, so
+// its buffer takes the stage four ahead (12 MFMA steps' time for the loads to
+// land).  The ring runs on over tile borders.
+template <int WB, int MODE>
+__global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(OrthArgs g) {
+  constexpr bool kSym = MODE <= kMul;
+  constexpr bool kTr = !kSym;
+  constexpr int TB = 2 * WB;
+  constexpr int kOpBytes = TB * 2048;               // one operand of a stage
+  constexpr int kStage = 2 * kOpBytes;
+  constexpr int kLoads = 2 * WB;                    // loads per wave and stage
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kONS * kStage + 4 * 4096];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+  const int G = gridDim.x;
+  const int mt = (g.mb + TB - 1) / TB, nt = (g.nb + TB - 1) / TB;
+  const int per_mat = kSym ? mt * (mt + 1) / 2 : mt * nt;
+  const int total = per_mat * g.count;
+  const int nkb = g.K / kOBK;
+
+  const int xcd = blockIdx.x % kOXcds, in_xcd = blockIdx.x / kOXcds;
+  auto tile_at = [&](int r) -> int {
+    const int base = r * G;
+    if (base >= total) return -1;
+    const int n = min(G, total - base);
+    const int q = n / kOXcds, rem = n % kOXcds;
+    if (in_xcd >= q + (xcd < rem ? 1 : 0)) return -1;
+    return base + xcd * q + min(xcd, rem) + in_xcd;
+  };
+
+  struct Tile {
+    int mat, rb, cb;                                // first row block and column block
+  };
+  // Sources of this wave's loads: kPtr pointers of 2 KB pieces for each
+  // operand (WB == 1: 1 KB), advanced stage by stage through the tile.
+  constexpr int kPtr = WB > 1 ? WB / 2 : 1;
+  const unsigned char* src[2 * kPtr];
+  auto locate = [&](int ti) __attribute__((always_inline)) {
+    Tile t;
+    t.mat = ti / per_mat;
+    const int l = ti - t.mat * per_mat;
+    int i, j;
+    if constexpr (kSym) {
+      i = static_cast<int>((sqrtf(8.0f * l + 1.0f) - 1.0f) * 0.5f);
+      while (i * (i + 1) / 2 > l) --i;
+      while ((i + 1) * (i + 2) / 2 <= l) ++i;
+      j = l - i * (i + 1) / 2;
+    } else {
+      // column tiles vary slowly: the tiles that run together share x's columns
+      j = l / mt;
+      i = l - j * mt;
+    }
+    t.mat = __builtin_amdgcn_readfirstlane(t.mat);
+    t.rb = __builtin_amdgcn_readfirstlane(i * TB);
+    t.cb = __builtin_amdgcn_readfirstlane(j * TB);
+    return t;
+  };
+  auto point = [&](const Tile& t) __attribute__((always_inline)) {
+    const OrthJob& jb = g.job;
+    const unsigned char* p = reinterpret_cast<const unsigned char*>(jb.p + t.mat * g.p_stride);
+    const unsigned char* q = reinterpret_cast<const unsigned char*>(jb.q + t.mat * g.q_stride);
+#pragma unroll
+    for (int k = 0; k < kPtr; ++k) {
+      // kilobyte of the operand's stage; blocks past the matrix repeat its
+      // last one (in bounds, never stored)
+      const int lin = WB > 1 ? wave * WB + 2 * k : wave;
+      const int rb = min(t.rb + (lin >> 1), g.mb - 1), cb = min(t.cb + (lin >> 1), g.nb - 1);
+      src[k] = uniform(p + (static_cast<size_t>(rb) * (g.K >> 4) + (lin & 1)) * 1024);
+      src[kPtr + k] = uniform(q + (kTr ? static_cast<size_t>(2 * cb + (lin & 1)) * 1024
+                                       : (static_cast<size_t>(cb) * (g.K >> 4) + (lin & 1)) * 1024));
+    }
+  };
+  const uint32_t q_step = kTr ? static_cast<uint32_t>(g.nb) * 2048u : 2048u;   // bytes a stage advances q
+  auto advance = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kPtr; ++k) {
+      src[k] = uniform(src[k] + 2048);
+      src[kPtr + k] = uniform(src[kPtr + k] + q_step);
+    }
+  };
+
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem) + wave * WB * 1024);
+  const uint32_t voff[2] = {static_cast<uint32_t>(lane) * 16u, static_cast<uint32_t>(lane) * 16u + 1024u};
+  // load k (0 .. 2 WB - 1) of the stage that src points at, into ring buffer buf
+  auto issue = [&](int buf, int k) __attribute__((always_inline)) {
+    const int o = k < WB ? 0 : 1, l = k - o * WB;   // operand, load of the operand
+    const uint32_t lds = lds0 + static_cast<uint32_t>(buf * kStage + o * kOpBytes + l * 1024);
+    dma_run(src[o * kPtr + l / 2], voff[l & 1], __builtin_amdgcn_readfirstlane(lds));
+  };
+
+  typedef f16x8 Frag[2 * WB];
+  const uint32_t run0 = static_cast<uint32_t>(run_off(lane & 31, lane >> 5, 0));
+  const uint32_t run1 = static_cast<uint32_t>(run_off(lane & 31, lane >> 5, 1));
+  // operand k of a step: k < WB row block, else column block
+  auto read_op = [&](int buf, int step, int k, Frag& f) __attribute__((always_inline)) {
+    const unsigned char* s = smem + buf * kStage;
+    if (k < WB) {
+      f[k] = *reinterpret_cast<const f16x8*>(s + (2 * (wr * WB + k) + step) * 1024 + (step ? run1 : run0));
+    } else if constexpr (kTr) {
+      f[k] = tr_run(s + kOpBytes + (wc * WB + (k - WB)) * 2048, step, lane);
+    } else {
+      f[k] = *reinterpret_cast<const f16x8*>(s + kOpBytes + (2 * (wc * WB + (k - WB)) + step) * 1024 +
+                                             (step ? run1 : run0));
+    }
+  };
+
+  int round = 0;
+  int ti = tile_at(0);
+  if (ti < 0) return;
+  Tile cur = locate(ti);
+  point(cur);
+  int ring = 0;                                     // buffer of the next stage
+#pragma unroll
+  for (int s = 0; s < kONS; ++s) {
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) issue(s, k);
+    advance();
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm((kONS - 1) * kLoads));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frag f0, f1;
+#pragma unroll
+  for (int k = 0; k < 2 * WB; ++k) read_op(0, 0, k, f0);
+
+  while (ti >= 0) {
+    f32x16 acc[WB][WB];
+#pragma unroll
+    for (int i = 0; i < WB; ++i)
+#pragma unroll
+      for (int j = 0; j < WB; ++j) acc[i][j] = f32x16{0.f};
+
+    auto step = [&](const Frag& f, auto&& op) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < WB; ++i)
+#pragma unroll
+        for (int j = 0; j < WB; ++j) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[WB + j], f[i], acc[i][j], 0, 0, 0);
+          op(WB * i + j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+      for (int k = WB * WB; k < 2 * WB; ++k) op(k);
+    };
+    constexpr int kOps = WB * WB > 2 * WB ? WB * WB : 2 * WB;
+    constexpr int kEvery = kOps / (2 * WB);         // one operand read (and load) per so many MFMAs
+
+    auto stage = [&]() __attribute__((always_inline)) {
+      const int b0 = ring;
+      const int b1 = (ring + 1) & (kONS - 1);
+      step(f0, [&](int k) __attribute__((always_inline)) {
+        if (k % kEvery == 0) read_op(b0, 1, k / kEvery, f1);
+      });
+      // the next stage has landed once only the two stages issued after it
+      // fly (stores of the previous tile, issued later still, only make this
+      // wait longer)
+      __builtin_amdgcn_s_waitcnt(wait_vm(2 * kLoads));
+      __builtin_amdgcn_s_waitcnt(kWaitLds);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      step(f1, [&](int k) __attribute__((always_inline)) {
+        if (k % kEvery == 0) read_op(b1, 0, k / kEvery, f0);
+        if (k % kEvery == kEvery - 1) issue(b0, k / kEvery);
+      });
+      advance();
+      ring = b1;
+    };
+    for (int x = nkb - kONS; x > 0; --x) stage();
+    // the last stages load the next tile's first ones (behind the last tile:
+    // this tile's again, never used, so that every wait counts the same)
+    const int tn = tile_at(round + 1);
+    const Tile nxt = locate(max(tn, 0));
+    point(tn >= 0 ? nxt : cur);
+    for (int x = kONS; x > 0; --x) stage();
+
+    // ---- epilogue
+    const OrthJob& jb = g.job;
+    unsigned char* stg = smem + kONS * kStage + wave * 4096;
+    const int r = lane & 31, h = lane >> 5;
+    const size_t o16 = static_cast<size_t>(2 * g.nb);              // 16-column blocks per output row block
+    const float* dp = jb.dp + static_cast<size_t>(cur.mat) * g.d_stride;
+#pragma unroll
+    for (int i = 0; i < WB; ++i) {
+      const int rb = cur.rb + wr * WB + i;
+      if (rb >= g.mb) continue;
+      const float dpi = MODE == kGram ? 0.0f : dp[32 * rb + r];
+#pragma unroll
+      for (int j = 0; j < WB; ++j) {
+        const int cb = cur.cb + wc * WB + j;
+        if (cb >= g.nb) continue;
+        const bool diag = kSym && rb == cb;
+        // read this block's accumulators only now: without the (empty) asm the
+        // compiler copies all of them out of the AGPRs at once, and spills
+        if constexpr (WB == 4) asm volatile("" : "+a"(acc[i][j]));
+        // 8 consecutive columns a lane: 16 p + 8 h + 0..7
+        float v[2][8];
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * p + e]),
+                                                             __float_as_uint(acc[i][j][8 * p + 4 + e]), false, false);
+            v[p][e] = __uint_as_float(sw[0]);
+            v[p][4 + e] = __uint_as_float(sw[1]);
+          }
+        f16x8 w[2], wl[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const size_t blk = (static_cast<size_t>(rb) * o16 + 2 * cb + p) * 512 + (run_off(r, h, p) >> 1);
+          if constexpr (MODE == kGram) {
+            const float f = jb.so / (jb.sp * jb.sq);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[p][e] = static_cast<_Float16>(v[p][e] * f);
+          } else if constexpr (MODE == kPoly) {
+            // c R^2 + b R: c (R R + (d_i + d_j) R_ij) + b R_ij off the diagonal
+            const f16x8 m = *reinterpret_cast<const f16x8*>(jb.q + cur.mat * g.q_stride + blk);
+            const float* dq = dp + 32 * cb + 16 * p + 8 * h;
+            const float f = kC * jb.so / (jb.sp * jb.sq), f1 = jb.so / jb.sq;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[p][e] = static_cast<_Float16>(v[p][e] * f +
+                                              (kC * (dpi + dq[e]) + kB) * (f1 * static_cast<float>(m[e])));
+          } else if constexpr (MODE == kMul) {
+            const f16x8 mq = *reinterpret_cast<const f16x8*>(jb.q + cur.mat * g.q_stride + blk);
+            const f16x8 mp = *reinterpret_cast<const f16x8*>(jb.p + cur.mat * g.p_stride + blk);
+            const float* dq = jb.dq + static_cast<size_t>(cur.mat) * g.d_stride + 32 * cb + 16 * p + 8 * h;
+            const float f = jb.so / (jb.sp * jb.sq), fq = jb.so / jb.sq, fp = jb.so / jb.sp;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[p][e] = static_cast<_Float16>(v[p][e] * f + dpi * (fq * static_cast<float>(mq[e])) +
+                                              dq[e] * (fp * static_cast<float>(mp[e])));
+          } else {
+            const f16x8 xh = *reinterpret_cast<const f16x8*>(jb.q + cur.mat * g.q_stride + blk);
+            const f16x8 xl = *reinterpret_cast<const f16x8*>(jb.lo + cur.mat * g.q_stride + blk);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float y = v[p][e] * (1.0f / kSQ) +
+                              dpi * (static_cast<float>(xh[e]) + static_cast<float>(xl[e]));
+              v[p][e] = y;
+              if constexpr (MODE == kApply) {
+                w[p][e] = static_cast<_Float16>(y);
+                wl[p][e] = static_cast<_Float16>(y - static_cast<float>(w[p][e]));
+              }
+            }
+          }
+          if constexpr (kSym) {
+            if (diag) {
+              const int e = r - 16 * p - 8 * h;     // this lane's diagonal element
+              if (e >= 0 && e < 8) {
+                float a = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  a = k == e ? v[p][k] : a;
+                  w[p][k] = k == e ? static_cast<_Float16>(0.0f) : w[p][k];
+                }
+                a /= jb.sp * jb.sq;
+                float d;
+                if constexpr (MODE == kGram) d = a;
+                else if constexpr (MODE == kPoly) d = kA + kB * dpi + kC * (a + dpi * dpi);
+                else d = a + dpi * (jb.dq + static_cast<size_t>(cur.mat) * g.d_stride)[32 * cb + r];
+                jb.dout[static_cast<size_t>(cur.mat) * g.d_stride + 32 * rb + r] = d;
+              }
+            }
+          }
+          if constexpr (MODE != kFinal)
+            *reinterpret_cast<f16x8*>(jb.out + cur.mat * g.out_stride + blk) = w[p];
+          if constexpr (MODE == kApply)
+            *reinterpret_cast<f16x8*>(jb.out_lo + cur.mat * g.out_stride + blk) = wl[p];
+        }
+        if constexpr (kSym) {
+          if (cur.rb != cur.cb) {                   // the mirror image of a tile below the diagonal
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              *reinterpret_cast<f16x8*>(stg + 1024 * p + run_off(r, h, p)) = w[p];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              const f16x8 t = tr_run(stg, kk, lane);
+              *reinterpret_cast<f16x8*>(jb.out + cur.mat * g.out_stride +
+                                        (static_cast<size_t>(cb) * o16 + 2 * rb + kk) * 512 +
+                                        (run_off(r, h, kk) >> 1)) = t;
+            }
+          }
+        }
+        if constexpr (MODE == kFinal) {
+          const float f = g.scale / kSX;
+          typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+          u16x8 o[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[p][e] = f32_to_bf16(v[p][e] * f);
+          }
+          const size_t base = static_cast<size_t>(cur.mat) * g.rows * g.cols;
+          if (g.tall) {
+            // lane: row 32 cb + r of the caller's matrix, 8 of its columns
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              *reinterpret_cast<u16x8*>(stg + 1024 * p + run_off(r, h, p)) = o[p];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) o[kk] = __builtin_bit_cast(u16x8, tr_run(stg, kk, lane));
+          }
+          const int ur = 32 * (g.tall ? cb : rb) + r;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const int uc = 32 * (g.tall ? rb : cb) + 16 * p + 8 * h;
+            if (ur < g.rows) {
+              bf16_t* dst = g.user + base + static_cast<size_t>(ur) * g.cols + uc;
+              if (uc + 8 <= g.cols && (g.cols & 7) == 0) {
+                *reinterpret_cast<u16x8*>(dst) = o[p];
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (uc + e < g.cols) dst[e] = o[p][e];
+              }
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    ++round;
+    ti = tn;
+    cur = nxt;
+  }
+  // trailing loads land before the workgroup's LDS is given up
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+}
+
+// ------------------------------------------------------------------ input
+constexpr int kSumThreads = 256;
+constexpr int kSumElems = 16384;       // elements per workgroup of the sums
+
+template <typename T>
+__device__ __forceinline__ float load_elem(const T* p) {
+  if constexpr (sizeof(T) == 2) return bf16_to_f32(*p);
+  else return *p;
+}
+
+// the update before normalisation: g, or with momentum (already M <- mu M + g)
+// g + mu M or M
+template <typename T>
+__device__ __forceinline__ float update_elem(const T* g, const float* mom, float mu, bool nesterov, size_t i) {
+  if (mom == nullptr) return load_elem(g + i);
+  const float m = mom[i];
+  return nesterov ? fmaf(mu, m, load_elem(g + i)) : m;
+}
+
+// Sums of squares of the update, and the momentum's update.  In 64 bits: bf16
+// values reach 1e38, and their squares would leave fp32.
+template <typename T>
+__global__ __launch_bounds__(kSumThreads) void orth_sums_kernel(const T* g, float* mom, float mu, bool nesterov,
+                                                                int64_t elems, int parts, double* sums) {
+  __shared__ double red[kSumThreads / 64];
+  const size_t base = static_cast<size_t>(blockIdx.y) * elems;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSumElems;
+  double s = 0.0;
+  for (int64_t i = first + threadIdx.x; i < min(first + kSumElems, elems); i += kSumThreads) {
+    float u;
+    if (mom != nullptr) {
+      const float gv = load_elem(g + base + i);
+      const float m = fmaf(mu, mom[base + i], gv);
+      mom[base + i] = m;
+      u = nesterov ? fmaf(mu, m, gv) : m;
+    } else {
+      u = load_elem(g + base + i);
+    }
+    s += static_cast<double>(u) * u;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kSumThreads / 64; ++w) s += red[w];
+    sums[static_cast<size_t>(blockIdx.y) * parts + blockIdx.x] = s;
+  }
+}
+
+constexpr int kPackCols = 128;         // columns of x per workgroup (one row block)
+
+// x_0 = u / (|u|_F + eps) as fp16 hi + lo blocks, zero outside the matrix.
+template <typename T>
+__global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float* mom, float mu, bool nesterov,
+                                                        int rows, int cols, bool tall, float eps, int parts,
+                                                        const double* sums, int nb, _Float16* hi, _Float16* lo,
+                                                        int64_t x_stride) {
+  __shared__ __attribute__((aligned(16))) unsigned char buf[2][32 * kPackCols * 2];
+  __shared__ double s_inv;
+  const int mat = blockIdx.z, rb = blockIdx.y, c0 = blockIdx.x * kPackCols;
+  const int tid = threadIdx.x;
+  if (tid < 64) {
+    double s = 0.0;
+    for (int i = tid; i < parts; i += 64) s += sums[static_cast<size_t>(mat) * parts + i];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    if (tid == 0) {
+      const double n = sqrt(s) + static_cast<double>(eps);
+      // an infinity or a NaN anywhere makes the whole matrix NaN
+      s_inv = s < 1.0 / 0.0 ? (n > 0.0 ? kSX / n : 0.0) : 0.0 / 0.0;
+    }
+  }
+  __syncthreads();
+  const double inv = s_inv;
+  const int m = tall ? cols : rows, n = tall ? rows : cols;
+  const size_t base = static_cast<size_t>(mat) * rows * cols;
+  auto put = [&](int r, int c, float v) {        // element (r, c) of the 32 x kPackCols piece
+    const _Float16 a = static_cast<_Float16>(v);
+    const _Float16 b = static_cast<_Float16>(v - static_cast<float>(a));
+    const int at = (c >> 4) * 1024 + run_off(r, (c >> 3) & 1, (c >> 4) & 1) + (c & 7) * 2;
+    *reinterpret_cast<_Float16*>(buf[0] + at) = a;
+    *reinterpret_cast<_Float16*>(buf[1] + at) = b;
+  };
+  for (int i = tid; i < 32 * kPackCols; i += 256) {
+    // consecutive threads read consecutive elements of the caller's rows
+    const int r = tall ? i & 31 : i / kPackCols, c = tall ? i >> 5 : i % kPackCols;
+    const int gr = 32 * rb + r, gc = c0 + c;
+    float v = 0.0f;
+    if (gr < m && gc < n) {
+      const size_t at = base + (tall ? static_cast<size_t>(gc) * cols + gr : static_cast<size_t>(gr) * cols + gc);
+      v = static_cast<float>(update_elem(g, mom, mu, nesterov, at) * inv);
+    }
+    put(r, c, v);
+  }
+  __syncthreads();
+  const int blocks = min(kPackCols / 16, 2 * nb - c0 / 16);      // (a narrow matrix may end inside the piece)
+  const size_t at = mat * x_stride + (static_cast<size_t>(rb) * 2 * nb + c0 / 16) * 512;
+  for (int i = tid; i < blocks * 64; i += 256) {
+    *reinterpret_cast<u32x4*>(hi + at + i * 8) = *reinterpret_cast<const u32x4*>(buf[0] + i * 16);
+    *reinterpret_cast<u32x4*>(lo + at + i * 8) = *reinterpret_cast<const u32x4*>(buf[1] + i * 16);
+  }
+}
+
+// -------------------------------------------------------------- workspace
+struct OrthPlan {
+  int m, n, mp, np, parts;
+  size_t x_elems, s_elems;             // elements of one x and one symmetric matrix
+  size_t off_x[4], off_s[4], off_d[4], off_sums, bytes;
+};
+
+size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+OrthPlan plan_of(int64_t count, int rows, int cols) {
+  OrthPlan p{};
+  p.m = rows < cols ? rows : cols;
+  p.n = rows < cols ? cols : rows;
+  auto pad = [](int v) { return v <= kMinPad ? kMinPad : (v + 31) & ~31; };
+  p.mp = pad(p.m);
+  p.np = pad(p.n);
+  const int64_t elems = static_cast<int64_t>(rows) * cols;
+  p.parts = static_cast<int>((elems + kSumElems - 1) / kSumElems);
+  p.x_elems = static_cast<size_t>(p.mp) * p.np;
+  p.s_elems = static_cast<size_t>(p.mp) * p.mp;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += up256(bytes);
+    return o;
+  };
+  for (auto& o : p.off_x) o = take(count * p.x_elems * 2);
+  for (auto& o : p.off_s) o = take(count * p.s_elems * 2);
+  for (auto& o : p.off_d) o = take(static_cast<size_t>(count) * p.mp * 4);
+  p.off_sums = take(static_cast<size_t>(count) * p.parts * 8);
+  p.bytes = at;
+  return p;
+}
+
+// whether the first two steps are taken together
+bool paired(int m, int n, int steps) { return steps >= 2 && m >= 256 && 2 * n >= 3 * m; }
+
+template <int WB, int MODE>
+void launch_one(const OrthArgs& a, hipStream_t st) {
+  const int slots = WB == 4 ? 256 : 512;
+  const int mt = (a.mb + 2 * WB - 1) / (2 * WB), nt = (a.nb + 2 * WB - 1) / (2 * WB);
+  const int64_t tiles = static_cast<int64_t>(MODE <= kMul ? mt * (mt + 1) / 2 : mt * nt) * a.count;
+  const int grid = static_cast<int>(tiles < slots ? tiles : slots);
+  orth_gemm_kernel<WB, MODE><<<(grid + 7) / 8 * 8, kOThreads, 0, st>>>(a);
+}
+
+template <int MODE>
+void launch_mode(const OrthArgs& a, hipStream_t st) {
+  const int mt = (a.mb + 7) / 8, nt = (a.nb + 7) / 8;
+  const int64_t tiles = static_cast<int64_t>(MODE <= kMul ? mt * (mt + 1) / 2 : mt * nt) * a.count;
+  if (tiles >= 192) launch_one<4, MODE>(a, st);
+  else launch_one<2, MODE>(a, st);
+}
+
+}  // namespace
+
+size_t orth_workspace_bytes(int64_t count, int rows, int cols) { return plan_of(count, rows, cols).bytes; }
+
+hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, const void* g, float* mom, float mu,
+                                bool nesterov, int steps, float eps, float scale, bf16_t* out, void* workspace,
+                                hipStream_t st) {
+  const OrthPlan p = plan_of(count, rows, cols);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  _Float16* X[4];
+  _Float16* S[4];
+  float* D[4];
+  for (int i = 0; i < 4; ++i) X[i] = reinterpret_cast<_Float16*>(ws + p.off_x[i]);
+  for (int i = 0; i < 4; ++i) S[i] = reinterpret_cast<_Float16*>(ws + p.off_s[i]);
+  for (int i = 0; i < 4; ++i) D[i] = reinterpret_cast<float*>(ws + p.off_d[i]);
+  double* sums = reinterpret_cast<double*>(ws + p.off_sums);
+  const bool tall = rows > cols;
+  const int64_t elems = static_cast<int64_t>(rows) * cols;
+  const int n = static_cast<int>(count);
+  const dim3 gs(p.parts, n), gp((p.np + kPackCols - 1) / kPackCols, p.mp / 32, n);
+  if (bf16) {
+    const bf16_t* gb = static_cast<const bf16_t*>(g);
+    orth_sums_kernel<bf16_t><<<gs, kSumThreads, 0, st>>>(gb, mom, mu, nesterov, elems, p.parts, sums);
+    orth_pack_kernel<bf16_t><<<gp, 256, 0, st>>>(gb, mom, mu, nesterov, rows, cols, tall, eps, p.parts, sums,
+                                                 p.np / 32, X[0], X[1], p.x_elems);
+  } else {
+    const float* gf = static_cast<const float*>(g);
+    orth_sums_kernel<float><<<gs, kSumThreads, 0, st>>>(gf, mom, mu, nesterov, elems, p.parts, sums);
+    orth_pack_kernel<float><<<gp, 256, 0, st>>>(gf, mom, mu, nesterov, rows, cols, tall, eps, p.parts, sums,
+                                                p.np / 32, X[0], X[1], p.x_elems);
+  }
+
+  OrthArgs base{};
+  base.count = n;
+  base.mb = p.mp / 32;
+  base.d_stride = p.mp;
+  base.rows = rows;
+  base.cols = cols;
+  base.tall = tall;
+  base.scale = scale;
+  base.user = out;
+  const int64_t xs = static_cast<int64_t>(p.x_elems), ss = static_cast<int64_t>(p.s_elems);
+  int xi = 0;                                   // x lives in X[xi], X[xi + 1]
+  enum { R = 0, T = 1, U = 2, V = 3 };
+  auto sym_args = [&] {
+    OrthArgs a = base;
+    a.nb = p.mp / 32;
+    a.K = p.mp;
+    a.p_stride = a.q_stride = a.out_stride = ss;
+    return a;
+  };
+  auto gram = [&] {
+    OrthArgs a = sym_args();
+    a.K = p.np;
+    a.p_stride = a.q_stride = xs;
+    a.job = {X[xi], X[xi], nullptr, nullptr, nullptr, S[R], nullptr, D[R], kSX, kSX, kSX};
+    launch_mode<kGram>(a, st);
+  };
+  auto poly = [&](int q) {                      // S[q] = Q(S[R])
+    OrthArgs a = sym_args();
+    a.job = {S[R], S[R], nullptr, D[R], D[R], S[q], nullptr, D[q], kSX, kSX, kSQ};
+    launch_mode<kPoly>(a, st);
+  };
+  auto product = [&](int pm, float sp, int qm, float sq, int om, float so) -> OrthJob {
+    return {S[pm], S[qm], nullptr, D[pm], D[qm], S[om], nullptr, D[om], sp, sq, so};
+  };
+  auto mul = [&](const OrthJob& j) {
+    OrthArgs a = sym_args();
+    a.job = j;
+    launch_mode<kMul>(a, st);
+  };
+  auto apply = [&](int q, bool last) {          // x <- S[q] x
+    OrthArgs a = base;
+    a.nb = p.np / 32;
+    a.K = p.mp;
+    a.p_stride = ss;
+    a.q_stride = a.out_stride = xs;
+    a.job = {S[q], X[xi], X[xi + 1], D[q], nullptr, X[xi ^ 2], X[(xi ^ 2) + 1], nullptr, kSQ, kSX, kSX};
+    if (last) launch_mode<kFinal>(a, st);
+    else launch_mode<kApply>(a, st);
+    xi ^= 2;
+  };
+
+  int left = steps;
+  if (paired(p.m, p.n, steps)) {
+    gram();
+    poly(U);                                    // Q1
+    mul(product(U, kSQ, R, kSX, T, kSX));       // T = Q1 R
+    mul(product(T, kSX, U, kSQ, R, kSX));       // R' = T Q1
+    poly(V);                                    // Q2
+    mul(product(V, kSQ, U, kSQ, T, kSQ));       // Q2 Q1
+    left -= 2;
+    apply(T, left == 0);
+  }
+  while (left > 0) {
+    gram();
+    poly(U);
+    apply(U, --left == 0);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe
