@@ -314,6 +314,60 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       ring = b1;
     };
     for (int x = nkb - kONS; x > 0; --x) stage();
+    // ---- what the epilogue reads beside the accumulators (block (rb, cb) of
+    // the operands, diagonals) is loaded kAhead blocks ahead, the first ones
+    // before the tile's last stages
+    constexpr int kBlocks = WB * WB, kAhead = 4;
+    const size_t o16 = static_cast<size_t>(2 * g.nb);              // 16-column blocks per output row block
+    const int r = lane & 31, h = lane >> 5;
+    auto row_block = [&](int i) { return cur.rb + wr * WB + i; };
+    auto col_block = [&](int j) { return cur.cb + wc * WB + j; };
+    // byte offset of block (rb, cb)'s 2 KB (two 16-column blocks)
+    auto at_block = [&](int rb, int cb) { return (static_cast<size_t>(rb) * o16 + 2 * cb) * 1024; };
+    // blocks q go down the tile's columns (kFinal: along the caller's rows)
+    const bool across = MODE == kFinal && !g.tall;
+    struct Ahead {
+      f16x8 a[2], b[2];
+    } pre[kAhead];
+    float dp[WB], dq[MODE == kPoly || MODE == kMul ? 2 : 1][16];
+    auto run_of = [&](const _Float16* m, int64_t stride, int rb, int cb, f16x8 (&v)[2]) __attribute__((always_inline)) {
+      const unsigned char* p = uniform(reinterpret_cast<const unsigned char*>(m + cur.mat * stride) + at_block(rb, cb));
+      v[0] = *reinterpret_cast<const f16x8*>(p + run0);
+      v[1] = *reinterpret_cast<const f16x8*>(p + 1024 + run1);
+    };
+    auto fetch = [&](int q) __attribute__((always_inline)) {
+      if constexpr (MODE != kGram) {
+        // (blocks past the matrix: its last one, in bounds and not used)
+        const int rb = min(row_block(across ? q / WB : q % WB), g.mb - 1);
+        const int cb = min(col_block(across ? q % WB : q / WB), g.nb - 1);
+        Ahead& e = pre[q % kAhead];
+        if constexpr (MODE == kMul) run_of(g.job.p, g.p_stride, rb, cb, e.b);
+        run_of(g.job.q, g.q_stride, rb, cb, e.a);
+        if constexpr (!kSym) run_of(g.job.lo, g.q_stride, rb, cb, e.b);
+      }
+    };
+    auto fetch_dq = [&](int j) __attribute__((always_inline)) {
+      if constexpr (MODE == kPoly || MODE == kMul) {
+        const float* d = uniform(g.job.dq + static_cast<size_t>(cur.mat) * g.d_stride +
+                                 32 * min(col_block(j), g.nb - 1));
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(d + 16 * p + 8 * h + 4 * k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dq[j & 1][8 * p + 4 * k + e] = v[e];
+          }
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < WB; ++i)
+      dp[i] = MODE == kGram ? 0.0f
+                            : g.job.dp[static_cast<size_t>(cur.mat) * g.d_stride + 32 * min(row_block(i), g.mb - 1) + r];
+    fetch_dq(0);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) fetch(q);
+
     // the last stages load the next tile's first ones (behind the last tile:
     // this tile's again, never used, so that every wait counts the same)
     const int tn = tile_at(round + 1);
@@ -324,66 +378,59 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     // ---- epilogue
     const OrthJob& jb = g.job;
     unsigned char* stg = smem + kONS * kStage + wave * 4096;
-    const int r = lane & 31, h = lane >> 5;
-    const size_t o16 = static_cast<size_t>(2 * g.nb);              // 16-column blocks per output row block
-    const float* dp = jb.dp + static_cast<size_t>(cur.mat) * g.d_stride;
+    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+    u16x8 ob[2][2];                                 // kFinal: the two blocks of a 64-element piece of rows
 #pragma unroll
-    for (int i = 0; i < WB; ++i) {
-      const int rb = cur.rb + wr * WB + i;
-      if (rb >= g.mb) continue;
-      const float dpi = MODE == kGram ? 0.0f : dp[32 * rb + r];
-#pragma unroll
-      for (int j = 0; j < WB; ++j) {
-        const int cb = cur.cb + wc * WB + j;
-        if (cb >= g.nb) continue;
-        const bool diag = kSym && rb == cb;
+    for (int q = 0; q < kBlocks; ++q) {
+      const int i = MODE == kFinal ? q / WB : q % WB, j = MODE == kFinal ? q % WB : q / WB;
+      // (kFinal of a tall matrix: the same q goes down the columns)
+      auto block = [&](int bi, int bj, f32x16& c) __attribute__((always_inline)) {
         // read this block's accumulators only now: without the (empty) asm the
         // compiler copies all of them out of the AGPRs at once, and spills
-        if constexpr (WB == 4) asm volatile("" : "+a"(acc[i][j]));
+        if constexpr (WB == 4) asm volatile("" : "+a"(c));
+        const int rb = row_block(bi), cb = col_block(bj);
+        const bool inside = rb < g.mb && cb < g.nb;
+        const bool diag = kSym && rb == cb;
         // 8 consecutive columns a lane: 16 p + 8 h + 0..7
         float v[2][8];
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[i][j][8 * p + e]),
-                                                             __float_as_uint(acc[i][j][8 * p + 4 + e]), false, false);
+            const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[8 * p + e]),
+                                                             __float_as_uint(c[8 * p + 4 + e]), false, false);
             v[p][e] = __uint_as_float(sw[0]);
             v[p][4 + e] = __uint_as_float(sw[1]);
           }
+        const float dpi = dp[bi];
+        const Ahead& pe = pre[q % kAhead];
         f16x8 w[2], wl[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const size_t blk = (static_cast<size_t>(rb) * o16 + 2 * cb + p) * 512 + (run_off(r, h, p) >> 1);
           if constexpr (MODE == kGram) {
             const float f = jb.so / (jb.sp * jb.sq);
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[p][e] = static_cast<_Float16>(v[p][e] * f);
           } else if constexpr (MODE == kPoly) {
             // c R^2 + b R: c (R R + (d_i + d_j) R_ij) + b R_ij off the diagonal
-            const f16x8 m = *reinterpret_cast<const f16x8*>(jb.q + cur.mat * g.q_stride + blk);
-            const float* dq = dp + 32 * cb + 16 * p + 8 * h;
             const float f = kC * jb.so / (jb.sp * jb.sq), f1 = jb.so / jb.sq;
+            const float u = fmaf(kC * f1, dpi, kB * f1);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              w[p][e] = static_cast<_Float16>(v[p][e] * f +
-                                              (kC * (dpi + dq[e]) + kB) * (f1 * static_cast<float>(m[e])));
+              w[p][e] = static_cast<_Float16>(
+                  fmaf(static_cast<float>(pe.a[p][e]), fmaf(kC * f1, dq[bj & 1][8 * p + e], u), v[p][e] * f));
           } else if constexpr (MODE == kMul) {
-            const f16x8 mq = *reinterpret_cast<const f16x8*>(jb.q + cur.mat * g.q_stride + blk);
-            const f16x8 mp = *reinterpret_cast<const f16x8*>(jb.p + cur.mat * g.p_stride + blk);
-            const float* dq = jb.dq + static_cast<size_t>(cur.mat) * g.d_stride + 32 * cb + 16 * p + 8 * h;
-            const float f = jb.so / (jb.sp * jb.sq), fq = jb.so / jb.sq, fp = jb.so / jb.sp;
+            const float f = jb.so / (jb.sp * jb.sq), fp = jb.so / jb.sp, u = dpi * (jb.so / jb.sq);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              w[p][e] = static_cast<_Float16>(v[p][e] * f + dpi * (fq * static_cast<float>(mq[e])) +
-                                              dq[e] * (fp * static_cast<float>(mp[e])));
+              w[p][e] = static_cast<_Float16>(
+                  fmaf(static_cast<float>(pe.b[p][e]), dq[bj & 1][8 * p + e] * fp,
+                       fmaf(static_cast<float>(pe.a[p][e]), u, v[p][e] * f)));
           } else {
-            const f16x8 xh = *reinterpret_cast<const f16x8*>(jb.q + cur.mat * g.q_stride + blk);
-            const f16x8 xl = *reinterpret_cast<const f16x8*>(jb.lo + cur.mat * g.q_stride + blk);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float y = v[p][e] * (1.0f / kSQ) +
-                              dpi * (static_cast<float>(xh[e]) + static_cast<float>(xl[e]));
+              const float y = fmaf(static_cast<float>(pe.a[p][e]), dpi,
+                                   fmaf(static_cast<float>(pe.b[p][e]), dpi, v[p][e] * (1.0f / kSQ)));
               v[p][e] = y;
               if constexpr (MODE == kApply) {
                 w[p][e] = static_cast<_Float16>(y);
@@ -391,8 +438,12 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
               }
             }
           }
-          if constexpr (kSym) {
-            if (diag) {
+        }
+        if (q + kAhead < kBlocks) fetch(q + kAhead);
+        if constexpr (kSym) {
+          if (diag) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
               const int e = r - 16 * p - 8 * h;     // this lane's diagonal element
               if (e >= 0 && e < 8) {
                 float a = 0.0f;
@@ -405,66 +456,92 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
                 float d;
                 if constexpr (MODE == kGram) d = a;
                 else if constexpr (MODE == kPoly) d = kA + kB * dpi + kC * (a + dpi * dpi);
-                else d = a + dpi * (jb.dq + static_cast<size_t>(cur.mat) * g.d_stride)[32 * cb + r];
-                jb.dout[static_cast<size_t>(cur.mat) * g.d_stride + 32 * rb + r] = d;
+                else d = a + dpi * (jb.dq + static_cast<size_t>(cur.mat) * g.d_stride)[32 * min(cb, g.nb - 1) + r];
+                if (inside) jb.dout[static_cast<size_t>(cur.mat) * g.d_stride + 32 * rb + r] = d;
               }
             }
           }
-          if constexpr (MODE != kFinal)
-            *reinterpret_cast<f16x8*>(jb.out + cur.mat * g.out_stride + blk) = w[p];
-          if constexpr (MODE == kApply)
-            *reinterpret_cast<f16x8*>(jb.out_lo + cur.mat * g.out_stride + blk) = wl[p];
         }
-        if constexpr (kSym) {
-          if (cur.rb != cur.cb) {                   // the mirror image of a tile below the diagonal
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-              *reinterpret_cast<f16x8*>(stg + 1024 * p + run_off(r, h, p)) = w[p];
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const f16x8 t = tr_run(stg, kk, lane);
-              *reinterpret_cast<f16x8*>(jb.out + cur.mat * g.out_stride +
-                                        (static_cast<size_t>(cb) * o16 + 2 * rb + kk) * 512 +
-                                        (run_off(r, h, kk) >> 1)) = t;
+        if constexpr (MODE != kFinal) {
+          if (inside) {
+            auto put = [&](_Float16* m, int row, int col, const f16x8 (&x)[2]) __attribute__((always_inline)) {
+              unsigned char* p = uniform(reinterpret_cast<unsigned char*>(m + cur.mat * g.out_stride) + at_block(row, col));
+              *reinterpret_cast<f16x8*>(p + run0) = x[0];
+              *reinterpret_cast<f16x8*>(p + 1024 + run1) = x[1];
+            };
+            put(jb.out, rb, cb, w);
+            if constexpr (MODE == kApply) put(jb.out_lo, rb, cb, wl);
+            if constexpr (kSym) {
+              if (cur.rb != cur.cb) {               // the mirror image of a tile below the diagonal
+                *reinterpret_cast<f16x8*>(stg + run0) = w[0];
+                *reinterpret_cast<f16x8*>(stg + 1024 + run1) = w[1];
+                const f16x8 t[2] = {tr_run(stg, 0, lane), tr_run(stg, 1, lane)};
+                put(jb.out, cb, rb, t);
+              }
             }
           }
-        }
-        if constexpr (MODE == kFinal) {
+        } else {
           const float f = g.scale / kSX;
-          typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-          u16x8 o[2];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[p][e] = f32_to_bf16(v[p][e] * f);
-          }
-          const size_t base = static_cast<size_t>(cur.mat) * g.rows * g.cols;
+            for (int e = 0; e < 8; ++e) ob[q & 1][p][e] = f32_to_bf16(v[p][e] * f);
+        }
+      };
+      if constexpr (MODE != kFinal) {
+        if (i == 0 && j + 1 < WB) fetch_dq(j + 1);
+        block(i, j, acc[i][j]);
+      } else if (!g.tall) {
+        block(i, j, acc[i][j]);
+      } else {
+        block(j, i, acc[j][i]);
+      }
+      if constexpr (MODE == kFinal) {
+        // two blocks make 64 consecutive elements of 32 of the caller's rows:
+        // through LDS (chunks XOR-swizzled by row / 2), then whole 128-byte
+        // segments, 8 rows a store
+        if ((q & 1) == 1) {
           if (g.tall) {
             // lane: row 32 cb + r of the caller's matrix, 8 of its columns
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-              *reinterpret_cast<u16x8*>(stg + 1024 * p + run_off(r, h, p)) = o[p];
+            for (int t = 0; t < 2; ++t) {
+              *reinterpret_cast<u16x8*>(stg + 2048 * t + run0) = ob[t][0];
+              *reinterpret_cast<u16x8*>(stg + 2048 * t + 1024 + run1) = ob[t][1];
+            }
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) o[kk] = __builtin_bit_cast(u16x8, tr_run(stg, kk, lane));
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) ob[t][p] = __builtin_bit_cast(u16x8, tr_run(stg + 2048 * t, p, lane));
           }
-          const int ur = 32 * (g.tall ? cb : rb) + r;
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const int uc = 32 * (g.tall ? rb : cb) + 16 * p + 8 * h;
-            if (ur < g.rows) {
-              bf16_t* dst = g.user + base + static_cast<size_t>(ur) * g.cols + uc;
-              if (uc + 8 <= g.cols && (g.cols & 7) == 0) {
-                *reinterpret_cast<u16x8*>(dst) = o[p];
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+              *reinterpret_cast<u16x8*>(stg + r * 128 + (((4 * t + 2 * p + h) ^ ((r >> 1) & 7)) << 4)) = ob[t][p];
+          // first caller row and column of the piece
+          const int ur0 = 32 * (g.tall ? col_block(i) : row_block(i));
+          const int uc0 = 32 * (g.tall ? row_block(j - 1) : col_block(j - 1));
+          bf16_t* user = g.user + static_cast<size_t>(cur.mat) * g.rows * g.cols;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = 8 * k + (lane >> 3), ch = lane & 7;
+            const u32x4 x = *reinterpret_cast<const u32x4*>(stg + row * 128 + ((ch ^ ((row >> 1) & 7)) << 4));
+            const int ur = ur0 + row, uc = uc0 + 8 * ch;
+            if (ur < g.rows && uc < g.cols) {
+              bf16_t* dst = user + static_cast<size_t>(ur) * g.cols + uc;
+              typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+              if (uc + 8 <= g.cols) {
+                *reinterpret_cast<u32x4u*>(dst) = x;
               } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  if (uc + e < g.cols) dst[e] = o[p][e];
+                  if (uc + e < g.cols) dst[e] = static_cast<bf16_t>(x[e >> 1] >> (16 * (e & 1)));
               }
             }
           }
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
     ++round;
     ti = tn;
@@ -484,35 +561,70 @@ __device__ __forceinline__ float load_elem(const T* p) {
   else return *p;
 }
 
-// the update before normalisation: g, or with momentum (already M <- mu M + g)
-// g + mu M or M
 template <typename T>
-__device__ __forceinline__ float update_elem(const T* g, const float* mom, float mu, bool nesterov, size_t i) {
-  if (mom == nullptr) return load_elem(g + i);
-  const float m = mom[i];
-  return nesterov ? fmaf(mu, m, load_elem(g + i)) : m;
+__device__ __forceinline__ void store_f32x8(T* p, const float (&v)[8]) {
+  typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[4 * k + e]);
+    *reinterpret_cast<raw*>(p + 4 * k) = w;
+  }
 }
 
-// Sums of squares of the update, and the momentum's update.  In 64 bits: bf16
-// values reach 1e38, and their squares would leave fp32.
+// 8 consecutive elements from any element's address
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+  for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) {
+    const u32x4 w = *reinterpret_cast<const raw*>(p + 4 * k);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * k + e] = __uint_as_float(w[e]);
+    }
+  }
+}
+
+// Sums of squares of the update u = g (or, with momentum, M <- mu M + g and
+// u = g + mu M or M), 8 elements a thread at a time.  In 64 bits: bf16 values
+// reach 1e38, and their squares would leave fp32.
 template <typename T>
 __global__ __launch_bounds__(kSumThreads) void orth_sums_kernel(const T* g, float* mom, float mu, bool nesterov,
                                                                 int64_t elems, int parts, double* sums) {
   __shared__ double red[kSumThreads / 64];
   const size_t base = static_cast<size_t>(blockIdx.y) * elems;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kSumElems;
+  const int64_t end = min(first + kSumElems, elems);
   double s = 0.0;
-  for (int64_t i = first + threadIdx.x; i < min(first + kSumElems, elems); i += kSumThreads) {
-    float u;
+  auto one = [&](float gv, float& m) {
+    float u = gv;
     if (mom != nullptr) {
-      const float gv = load_elem(g + base + i);
-      const float m = fmaf(mu, mom[base + i], gv);
-      mom[base + i] = m;
+      m = fmaf(mu, m, gv);
       u = nesterov ? fmaf(mu, m, gv) : m;
-    } else {
-      u = load_elem(g + base + i);
     }
-    s += static_cast<double>(u) * u;
+    s = fma(static_cast<double>(u), static_cast<double>(u), s);
+  };
+#pragma unroll 2
+  for (int64_t i = first + 8 * threadIdx.x; i < end; i += 8 * kSumThreads) {
+    float v[8], m[8];
+    if (i + 8 <= end) {
+      load8(g + base + i, v);
+      if (mom != nullptr) load8(mom + base + i, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) one(v[e], m[e]);
+      if (mom != nullptr) store_f32x8(mom + base + i, m);
+    } else {
+      for (int e = 0; i + e < end; ++e) {
+        float x = mom != nullptr ? mom[base + i + e] : 0.0f;
+        one(load_elem(g + base + i + e), x);
+        if (mom != nullptr) mom[base + i + e] = x;
+      }
+    }
   }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
@@ -526,7 +638,9 @@ __global__ __launch_bounds__(kSumThreads) void orth_sums_kernel(const T* g, floa
 
 constexpr int kPackCols = 128;         // columns of x per workgroup (one row block)
 
-// x_0 = u / (|u|_F + eps) as fp16 hi + lo blocks, zero outside the matrix.
+// x_0 = u / (|u|_F + eps) as fp16 hi + lo blocks, zero outside the matrix.  The
+// piece of 32 x 128 is read along the caller's rows, 8 elements a thread,
+// scattered into blocks in LDS, and written as whole kilobytes.
 template <typename T>
 __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float* mom, float mu, bool nesterov,
                                                         int rows, int cols, bool tall, float eps, int parts,
@@ -536,38 +650,73 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
   __shared__ double s_inv;
   const int mat = blockIdx.z, rb = blockIdx.y, c0 = blockIdx.x * kPackCols;
   const int tid = threadIdx.x;
+  const size_t base = static_cast<size_t>(mat) * rows * cols;
+  // unit i of 2: 8 elements along the caller's rows, from (row, col) of x
+  constexpr int kUnits = 32 * kPackCols / 8 / 256;
+  float u[kUnits][8];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int i = tid + 256 * k;
+    const int r = tall ? 8 * (i & 3) : i / (kPackCols / 8), c = tall ? i >> 2 : 8 * (i % (kPackCols / 8));
+    const int gr = 32 * rb + r, gc = c0 + c;                       // element (gr, gc) of x
+    const int ur = tall ? gc : gr, uc = tall ? gr : gc;            // of the caller's matrix
+    const size_t at = base + static_cast<size_t>(ur) * cols + uc;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[k][e] = 0.0f;
+    if (ur < rows && uc < cols) {
+      float mv[8];
+      if (uc + 8 <= cols) {
+        load8(g + at, u[k]);
+        if (mom != nullptr) load8(mom + at, mv);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          u[k][e] = uc + e < cols ? load_elem(g + at + e) : 0.0f;
+          mv[e] = mom != nullptr && uc + e < cols ? mom[at + e] : 0.0f;
+        }
+      }
+      if (mom != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[k][e] = nesterov ? fmaf(mu, mv[e], u[k][e]) : mv[e];
+      }
+    }
+  }
   if (tid < 64) {
     double s = 0.0;
     for (int i = tid; i < parts; i += 64) s += sums[static_cast<size_t>(mat) * parts + i];
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
     if (tid == 0) {
-      const double n = sqrt(s) + static_cast<double>(eps);
+      const double norm = sqrt(s) + static_cast<double>(eps);
       // an infinity or a NaN anywhere makes the whole matrix NaN
-      s_inv = s < 1.0 / 0.0 ? (n > 0.0 ? kSX / n : 0.0) : 0.0 / 0.0;
+      s_inv = s < 1.0 / 0.0 ? (norm > 0.0 ? kSX / norm : 0.0) : 0.0 / 0.0;
     }
   }
   __syncthreads();
   const double inv = s_inv;
-  const int m = tall ? cols : rows, n = tall ? rows : cols;
-  const size_t base = static_cast<size_t>(mat) * rows * cols;
-  auto put = [&](int r, int c, float v) {        // element (r, c) of the 32 x kPackCols piece
-    const _Float16 a = static_cast<_Float16>(v);
-    const _Float16 b = static_cast<_Float16>(v - static_cast<float>(a));
-    const int at = (c >> 4) * 1024 + run_off(r, (c >> 3) & 1, (c >> 4) & 1) + (c & 7) * 2;
-    *reinterpret_cast<_Float16*>(buf[0] + at) = a;
-    *reinterpret_cast<_Float16*>(buf[1] + at) = b;
-  };
-  for (int i = tid; i < 32 * kPackCols; i += 256) {
-    // consecutive threads read consecutive elements of the caller's rows
-    const int r = tall ? i & 31 : i / kPackCols, c = tall ? i >> 5 : i % kPackCols;
-    const int gr = 32 * rb + r, gc = c0 + c;
-    float v = 0.0f;
-    if (gr < m && gc < n) {
-      const size_t at = base + (tall ? static_cast<size_t>(gc) * cols + gr : static_cast<size_t>(gr) * cols + gc);
-      v = static_cast<float>(update_elem(g, mom, mu, nesterov, at) * inv);
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    const int i = tid + 256 * k;
+    const int r = tall ? 8 * (i & 3) : i / (kPackCols / 8), c = tall ? i >> 2 : 8 * (i % (kPackCols / 8));
+    f16x8 a, b;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = static_cast<float>(u[k][e] * inv);
+      a[e] = static_cast<_Float16>(v);
+      b[e] = static_cast<_Float16>(v - static_cast<float>(a[e]));
     }
-    put(r, c, v);
+    if (!tall) {
+      const int at = (c >> 4) * 1024 + run_off(r, (c >> 3) & 1, (c >> 4) & 1);
+      *reinterpret_cast<f16x8*>(buf[0] + at) = a;
+      *reinterpret_cast<f16x8*>(buf[1] + at) = b;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int at = (c >> 4) * 1024 + run_off(r + e, (c >> 3) & 1, (c >> 4) & 1) + (c & 7) * 2;
+        *reinterpret_cast<_Float16*>(buf[0] + at) = a[e];
+        *reinterpret_cast<_Float16*>(buf[1] + at) = b[e];
+      }
+    }
   }
   __syncthreads();
   const int blocks = min(kPackCols / 16, 2 * nb - c0 / 16);      // (a narrow matrix may end inside the piece)
