@@ -26,12 +26,14 @@
 // directions far below the largest are amplified by a^5 = 485, and bf16's 8
 // bits would add noise of 1% to 30% of the result.  Two parts are kept finer,
 // at no product's cost:
-//   * a symmetric matrix M is stored as its off-diagonal part in fp16 and its
-//     diagonal d in fp32; (M + d)(N + e) = M N + d_i N_ij + M_ij e_j is joined
-//     in fp32 in the epilogue.  The polynomial of a nearly null direction is
-//     a I, whose rounding would otherwise be the largest error;
-//   * x is stored as fp16 hi + lo (22 bits); the products read hi, and the
-//     elementwise part d_i x_ij reads both.
+//   * a symmetric matrix is stored as M + diag(d): d the diagonal rounded to
+//     fp16, M the rest in fp16 (on the diagonal what d leaves).  (M + d)(N + e) =
+//     M N + d_i N_ij + M_ij e_j + d_i e_i is joined in fp32 in the epilogue.
+//     The polynomial of a nearly null direction is a I, whose rounding would
+//     otherwise be the largest error;
+//   * x is stored as fp16 hi + lo (22 bits).  M x and diag(d) x read hi (the
+//     latter as MFMAs with a diagonal operand, in the stage that holds the
+//     rows), the epilogue adds d_i lo_ij.
 // Powers of two keep fp16 away from its subnormals: x and R are stored times
 // 2^12 (|x|, |R| < 2), Q and Q2 Q1 times 2^8 (|Q2 Q1| <= a^2 = 12).
 //
@@ -49,6 +51,8 @@
 //     the same transposing read.
 // Rows and columns are padded with zeros to multiples of 32 (at least 128):
 // zero rows stay zero, and the padded diagonal of Q meets zero rows of x.
+#include <type_traits>
+
 #include "lds_dma.h"
 
 namespace moe {
@@ -199,7 +203,10 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       i = l - j * mt;
     }
     t.mat = __builtin_amdgcn_readfirstlane(t.mat);
-    t.rb = __builtin_amdgcn_readfirstlane(i * TB);
+    // x's row tiles are all whole: the last one starts early (its first rows
+    // are written twice, with the same bits), so that every row block of a
+    // wave has its stage
+    t.rb = __builtin_amdgcn_readfirstlane(kTr ? min(i * TB, g.mb - TB) : i * TB);
     t.cb = __builtin_amdgcn_readfirstlane(j * TB);
     return t;
   };
@@ -278,6 +285,13 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
 #pragma unroll
       for (int j = 0; j < WB; ++j) acc[i][j] = f32x16{0.f};
 
+    float dp[WB];                                   // the diagonal of the row operand at this lane's rows
+#pragma unroll
+    for (int i = 0; i < WB; ++i)
+      dp[i] = MODE == kGram ? 0.0f
+                            : g.job.dp[static_cast<size_t>(cur.mat) * g.d_stride +
+                                       32 * min(cur.rb + wr * WB + i, g.mb - 1) + (lane & 31)];
+
     auto step = [&](const Frag& f, auto&& op) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < WB; ++i)
@@ -293,12 +307,26 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     constexpr int kOps = WB * WB > 2 * WB ? WB * WB : 2 * WB;
     constexpr int kEvery = kOps / (2 * WB);         // one operand read (and load) per so many MFMAs
 
-    auto stage = [&]() __attribute__((always_inline)) {
+    // The diagonal's part of x <- P x: in the stage that holds the rows of row
+    // block i of the wave, its accumulators also take diag(e) times those rows
+    // (e is exact in fp16).
+    auto diagonal = [&](int i, int st, const Frag& f) __attribute__((always_inline)) {
+      f16x8 e;
+      const int at = (lane & 31) - 16 * st - 8 * (lane >> 5);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = k == at ? static_cast<_Float16>(dp[i] * kSQ) : static_cast<_Float16>(0.0f);
+#pragma unroll
+      for (int j = 0; j < WB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[WB + j], e, acc[i][j], 0, 0, 0);
+    };
+    auto stage = [&](auto own_tag) __attribute__((always_inline)) {
+      constexpr int own = decltype(own_tag)::value;   // row block whose rows the stage holds, or -1
       const int b0 = ring;
       const int b1 = (ring + 1) & (kONS - 1);
       step(f0, [&](int k) __attribute__((always_inline)) {
         if (k % kEvery == 0) read_op(b0, 1, k / kEvery, f1);
       });
+      if constexpr (own >= 0) diagonal(own, 0, f0);
       // the next stage has landed once only the two stages issued after it
       // fly (stores of the previous tile, issued later still, only make this
       // wait longer)
@@ -310,10 +338,10 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
         if (k % kEvery == 0) read_op(b1, 0, k / kEvery, f0);
         if (k % kEvery == kEvery - 1) issue(b0, k / kEvery);
       });
+      if constexpr (own >= 0) diagonal(own, 1, f1);
       advance();
       ring = b1;
     };
-    for (int x = nkb - kONS; x > 0; --x) stage();
     // ---- what the epilogue reads beside the accumulators (block (rb, cb) of
     // the operands, diagonals) is loaded kAhead blocks ahead, the first ones
     // before the tile's last stages
@@ -327,9 +355,9 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     // blocks q go down the tile's columns (kFinal: along the caller's rows)
     const bool across = MODE == kFinal && !g.tall;
     struct Ahead {
-      f16x8 a[2], b[2];
+      f16x8 a[2], b[MODE == kMul ? 2 : 1];
     } pre[kAhead];
-    float dp[WB], dq[MODE == kPoly || MODE == kMul ? 2 : 1][16];
+    float dq[MODE == kPoly || MODE == kMul ? 2 : 1][16];
     auto run_of = [&](const _Float16* m, int64_t stride, int rb, int cb, f16x8 (&v)[2]) __attribute__((always_inline)) {
       const unsigned char* p = uniform(reinterpret_cast<const unsigned char*>(m + cur.mat * stride) + at_block(rb, cb));
       v[0] = *reinterpret_cast<const f16x8*>(p + run0);
@@ -342,8 +370,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
         const int cb = min(col_block(across ? q % WB : q / WB), g.nb - 1);
         Ahead& e = pre[q % kAhead];
         if constexpr (MODE == kMul) run_of(g.job.p, g.p_stride, rb, cb, e.b);
-        run_of(g.job.q, g.q_stride, rb, cb, e.a);
-        if constexpr (!kSym) run_of(g.job.lo, g.q_stride, rb, cb, e.b);
+        run_of(kSym ? g.job.q : g.job.lo, g.q_stride, rb, cb, e.a);
       }
     };
     auto fetch_dq = [&](int j) __attribute__((always_inline)) {
@@ -360,20 +387,40 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
           }
       }
     };
-#pragma unroll
-    for (int i = 0; i < WB; ++i)
-      dp[i] = MODE == kGram ? 0.0f
-                            : g.job.dp[static_cast<size_t>(cur.mat) * g.d_stride + 32 * min(row_block(i), g.mb - 1) + r];
-    fetch_dq(0);
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) fetch(q);
-
-    // the last stages load the next tile's first ones (behind the last tile:
-    // this tile's again, never used, so that every wait counts the same)
+    // before the tile's last kONS stages, which load the next tile's first ones
+    // (behind the last tile: this tile's again, never used, so that every wait
+    // counts the same)
     const int tn = tile_at(round + 1);
     const Tile nxt = locate(max(tn, 0));
-    point(tn >= 0 ? nxt : cur);
-    for (int x = kONS; x > 0; --x) stage();
+    auto turn = [&]() __attribute__((always_inline)) {
+      fetch_dq(0);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) fetch(q);
+      point(tn >= 0 ? nxt : cur);
+    };
+    using None = std::integral_constant<int, -1>;
+    if constexpr (kSym) {
+      for (int x = kONS; x < nkb; ++x) stage(None{});
+      turn();
+#pragma unroll 1
+      for (int x = 0; x < kONS; ++x) stage(None{});
+    } else {
+      // the stages of the wave's own row blocks apart (no branch may hold
+      // MFMAs: the accumulators would leave their registers)
+      int x = 0;
+      auto one = [&](auto own_tag) __attribute__((always_inline)) {
+        if (x == nkb - kONS) turn();
+        stage(own_tag);
+        ++x;
+      };
+      const int own = cur.rb + wr * WB;
+      while (x < own) one(None{});
+      one(std::integral_constant<int, 0>{});
+      if constexpr (WB > 1) one(std::integral_constant<int, 1>{});
+      if constexpr (WB > 2) one(std::integral_constant<int, 2>{});
+      if constexpr (WB > 3) one(std::integral_constant<int, 3>{});
+      while (x < nkb) one(None{});
+    }
 
     // ---- epilogue
     const OrthJob& jb = g.job;
@@ -410,27 +457,24 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
           if constexpr (MODE == kGram) {
             const float f = jb.so / (jb.sp * jb.sq);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[p][e] = static_cast<_Float16>(v[p][e] * f);
+            for (int e = 0; e < 8; ++e) v[p][e] *= f;
           } else if constexpr (MODE == kPoly) {
             // c R^2 + b R: c (R R + (d_i + d_j) R_ij) + b R_ij off the diagonal
             const float f = kC * jb.so / (jb.sp * jb.sq), f1 = jb.so / jb.sq;
             const float u = fmaf(kC * f1, dpi, kB * f1);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              w[p][e] = static_cast<_Float16>(
-                  fmaf(static_cast<float>(pe.a[p][e]), fmaf(kC * f1, dq[bj & 1][8 * p + e], u), v[p][e] * f));
+              v[p][e] = fmaf(static_cast<float>(pe.a[p][e]), fmaf(kC * f1, dq[bj & 1][8 * p + e], u), v[p][e] * f);
           } else if constexpr (MODE == kMul) {
             const float f = jb.so / (jb.sp * jb.sq), fp = jb.so / jb.sp, u = dpi * (jb.so / jb.sq);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              w[p][e] = static_cast<_Float16>(
-                  fmaf(static_cast<float>(pe.b[p][e]), dq[bj & 1][8 * p + e] * fp,
-                       fmaf(static_cast<float>(pe.a[p][e]), u, v[p][e] * f)));
+              v[p][e] = fmaf(static_cast<float>(pe.b[p][e]), dq[bj & 1][8 * p + e] * fp,
+                             fmaf(static_cast<float>(pe.a[p][e]), u, v[p][e] * f));
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float y = fmaf(static_cast<float>(pe.a[p][e]), dpi,
-                                   fmaf(static_cast<float>(pe.b[p][e]), dpi, v[p][e] * (1.0f / kSQ)));
+              const float y = fmaf(static_cast<float>(pe.a[p][e]), dpi, v[p][e] * (1.0f / kSQ));
               v[p][e] = y;
               if constexpr (MODE == kApply) {
                 w[p][e] = static_cast<_Float16>(y);
@@ -442,25 +486,28 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
         if (q + kAhead < kBlocks) fetch(q + kAhead);
         if constexpr (kSym) {
           if (diag) {
+            // split into e, exact in fp16, and what is left of it
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              const int e = r - 16 * p - 8 * h;     // this lane's diagonal element
-              if (e >= 0 && e < 8) {
-                float a = 0.0f;
+              const int at = r - 16 * p - 8 * h;    // this lane's diagonal element
+              if (at >= 0 && at < 8) {
+                float d = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  a = k == e ? v[p][k] : a;
-                  w[p][k] = k == e ? static_cast<_Float16>(0.0f) : w[p][k];
-                }
-                a /= jb.sp * jb.sq;
-                float d;
-                if constexpr (MODE == kGram) d = a;
-                else if constexpr (MODE == kPoly) d = kA + kB * dpi + kC * (a + dpi * dpi);
-                else d = a + dpi * (jb.dq + static_cast<size_t>(cur.mat) * g.d_stride)[32 * min(cb, g.nb - 1) + r];
-                if (inside) jb.dout[static_cast<size_t>(cur.mat) * g.d_stride + 32 * rb + r] = d;
+                for (int e = 0; e < 8; ++e) d = e == at ? v[p][e] : d;
+                if constexpr (MODE == kPoly) d = fmaf(jb.so, fmaf(dpi, fmaf(kC, dpi, kB), kA), d);
+                if constexpr (MODE == kMul) d = fmaf(jb.so * dpi, jb.dq[static_cast<size_t>(cur.mat) * g.d_stride +
+                                                                       32 * min(cb, g.nb - 1) + r], d);
+                const float e16 = static_cast<float>(static_cast<_Float16>(d));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[p][e] = e == at ? d - e16 : v[p][e];
+                if (inside) jb.dout[static_cast<size_t>(cur.mat) * g.d_stride + 32 * rb + r] = e16 / jb.so;
               }
             }
           }
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[p][e] = static_cast<_Float16>(v[p][e]);
         }
         if constexpr (MODE != kFinal) {
           if (inside) {
@@ -777,7 +824,7 @@ template <int MODE>
 void launch_mode(const OrthArgs& a, hipStream_t st) {
   const int mt = (a.mb + 7) / 8, nt = (a.nb + 7) / 8;
   const int64_t tiles = static_cast<int64_t>(MODE <= kMul ? mt * (mt + 1) / 2 : mt * nt) * a.count;
-  if (tiles >= 192) launch_one<4, MODE>(a, st);
+  if (tiles >= 192 && a.mb >= 8) launch_one<4, MODE>(a, st);
   else launch_one<2, MODE>(a, st);
 }
 
