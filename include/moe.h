@@ -503,8 +503,8 @@ size_t moe_orthogonalize_workspace_bytes(int64_t count, int32_t rows, int32_t co
  * output NaN and touches no other.  Products run on fp16 operands with fp32
  * accumulation, held finer where the result needs it (error against 64 bits
  * about the rounding of the bf16 output).
- * rows * cols < 2^30, count <= 65535, count * rows * cols < 2^36 (else
- * MOE_ERR_UNSUPPORTED). */
+ * rows, cols <= 65536, rows * cols < 2^30, count <= 65535, count * rows * cols <
+ * 2^36 (else MOE_ERR_UNSUPPORTED). */
 int moe_orthogonalize(int64_t count, int32_t rows, int32_t cols, int32_t dtype, const void* g,
                       float* momentum, float mu, int32_t nesterov, int32_t steps, float eps, float scale,
                       void* out, void* workspace, size_t workspace_bytes, void* stream);

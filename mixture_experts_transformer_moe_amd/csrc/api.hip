@@ -626,6 +626,7 @@ int check_norm(int32_t kind, int64_t rows, int32_t cols, int32_t dtype) {
 int check_orth(int64_t count, int32_t rows, int32_t cols) {
   if (count < 0 || rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "negative count or size");
   const int64_t elems = static_cast<int64_t>(rows) * cols;
+  if (rows > 65536 || cols > 65536) return fail(MOE_ERR_UNSUPPORTED, "rows = %d, cols = %d: at most 65536", rows, cols);
   if (elems >= (int64_t{1} << 30)) return fail(MOE_ERR_UNSUPPORTED, "rows * cols = %lld >= 2^30", static_cast<long long>(elems));
   if (count > 65535) return fail(MOE_ERR_UNSUPPORTED, "count = %lld > 65535", static_cast<long long>(count));
   if (count * elems >= (int64_t{1} << 36)) return fail(MOE_ERR_UNSUPPORTED, "count * rows * cols >= 2^36");

@@ -66,9 +66,9 @@ constexpr float kSX = 4096.0f;        // stored scale of x and R
 constexpr float kSQ = 256.0f;         // stored scale of Q and products of Qs
 constexpr int kOThreads = 256;        // 4 waves, 2 x 2
 constexpr int kOBK = 32;              // K per stage
-constexpr int kONS = 4;               // stages of the ring
+constexpr int kStages = 4;            // stages of the ring
 constexpr int kOXcds = 8;
-constexpr int kMinPad = 128;          // smallest padded side: a tile has at least kONS stages
+constexpr int kMinPad = 128;          // smallest padded side: a tile has at least kStages stages
 
 enum { kGram = 0, kPoly = 1, kMul = 2, kApply = 3, kFinal = 4 };
 
@@ -141,6 +141,108 @@ __device__ __forceinline__ f16x8 tr_run(const unsigned char* b, int kk, int lane
 constexpr int wait_vm(int n) { return vmcnt_only(n > 63 ? 63 : n); }
 constexpr int kWaitLds = 15 | (7 << 4) | (0 << 8) | (3 << 14);     // lgkmcnt(0) only
 
+// Row and column tile of entry l of the tiles on and below the diagonal.
+__device__ __forceinline__ void triangle(int l, int& i, int& j) {
+  i = static_cast<int>((sqrtf(8.0f * l + 1.0f) - 1.0f) * 0.5f);
+  while (i * (i + 1) / 2 > l) --i;
+  while ((i + 1) * (i + 2) / 2 <= l) ++i;
+  j = l - i * (i + 1) / 2;
+}
+
+// 8 consecutive elements of an output row from their sums of products v, in the
+// output's stored scale.  a: the column operand's elements at this place (x's
+// low part in kApply and kFinal), b: the row operand's; dpi, dq: the operands'
+// diagonals at this row and these columns.
+template <int MODE>
+__device__ __forceinline__ void finish(float (&v)[8], const f16x8& a, const f16x8& b, float dpi, const float* dq,
+                                       const OrthJob& jb) {
+  if constexpr (MODE == kGram) {
+    const float f = jb.so / (jb.sp * jb.sq);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+  } else if constexpr (MODE == kPoly) {
+    // c R^2 + b R = c (M M + (d_i + d_j) M_ij) + b M_ij off the diagonal
+    const float f = kC * jb.so / (jb.sp * jb.sq), f1 = jb.so / jb.sq;
+    const float u = fmaf(kC * f1, dpi, kB * f1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(static_cast<float>(a[e]), fmaf(kC * f1, dq[e], u), v[e] * f);
+  } else if constexpr (MODE == kMul) {
+    const float f = jb.so / (jb.sp * jb.sq), fp = jb.so / jb.sp, u = dpi * (jb.so / jb.sq);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = fmaf(static_cast<float>(b[e]), dq[e] * fp, fmaf(static_cast<float>(a[e]), u, v[e] * f));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(static_cast<float>(a[e]), dpi, v[e] * (1.0f / kSQ));
+  }
+}
+
+// The diagonal element (at 0..7 of v) of a symmetric output: completed, then
+// split into a part exact in fp16, which is returned, and the rest, left in v.
+template <int MODE>
+__device__ __forceinline__ float split_diagonal(float (&v)[8], int at, float dpi, float dqi, float so) {
+  float d = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) d = e == at ? v[e] : d;
+  if constexpr (MODE == kPoly) d = fmaf(so, fmaf(dpi, fmaf(kC, dpi, kB), kA), d);
+  if constexpr (MODE == kMul) d = fmaf(so * dpi, dqi, d);
+  const float e16 = static_cast<float>(static_cast<_Float16>(d));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e == at ? d - e16 : v[e];
+  return e16 / so;
+}
+
+__device__ __forceinline__ f16x8 to_f16(const float (&v)[8]) {
+  f16x8 w;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = static_cast<_Float16>(v[e]);
+  return w;
+}
+
+// what rounding v to w left
+__device__ __forceinline__ f16x8 low_part(const float (&v)[8], const f16x8& w) {
+  f16x8 l;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) l[e] = static_cast<_Float16>(v[e] - static_cast<float>(w[e]));
+  return l;
+}
+
+__device__ __forceinline__ u32x4 to_bf16(const float (&v)[8], float f) {
+  u32x4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(v[2 * e] * f, v[2 * e + 1] * f);
+  return o;
+}
+
+// 8 elements to (row, col) of a matrix of the caller's (any element alignment)
+__device__ __forceinline__ void store_rows(bf16_t* matrix, int rows, int cols, int row, int col, const u32x4& x) {
+  if (row >= rows || col >= cols) return;
+  bf16_t* dst = matrix + static_cast<size_t>(row) * cols + col;
+  typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+  if (col + 8 <= cols) {
+    *reinterpret_cast<u32x4u*>(dst) = x;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (col + e < cols) dst[e] = static_cast<bf16_t>(x[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+__device__ __forceinline__ void store_user(const OrthArgs& g, int mat, int row, int col, const u32x4& x) {
+  store_rows(g.user + static_cast<size_t>(mat) * g.rows * g.cols, g.rows, g.cols, row, col, x);
+}
+
+// Halves of a lane's accumulator registers swapped with the other half wave's:
+// lane l gets columns 8 (l / 32) .. + 7 of the 16 whose 8 registers c points at.
+__device__ __forceinline__ void gather_columns(const float (&c)[8], float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[e]), __float_as_uint(c[4 + e]), false, false);
+    v[e] = __uint_as_float(sw[0]);
+    v[4 + e] = __uint_as_float(sw[1]);
+  }
+}
+
 // One product of the iteration.  A tile is TB x TB blocks of 32 (TB = 2 WB),
 // each wave owns WB x WB of them.  The symmetric modes compute the tiles on
 // and below the diagonal and store the mirror image of those below.
@@ -160,7 +262,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
   constexpr int kOpBytes = TB * 2048;               // one operand of a stage
   constexpr int kStage = 2 * kOpBytes;
   constexpr int kLoads = 2 * WB;                    // loads per wave and stage
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[kONS * kStage + 4 * 4096];
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kStages * kStage + 4 * 4096];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wr = wave >> 1, wc = wave & 1;
@@ -193,10 +295,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     const int l = ti - t.mat * per_mat;
     int i, j;
     if constexpr (kSym) {
-      i = static_cast<int>((sqrtf(8.0f * l + 1.0f) - 1.0f) * 0.5f);
-      while (i * (i + 1) / 2 > l) --i;
-      while ((i + 1) * (i + 2) / 2 <= l) ++i;
-      j = l - i * (i + 1) / 2;
+      triangle(l, i, j);
     } else {
       // column tiles vary slowly: the tiles that run together share x's columns
       j = l / mt;
@@ -266,12 +365,12 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
   point(cur);
   int ring = 0;                                     // buffer of the next stage
 #pragma unroll
-  for (int s = 0; s < kONS; ++s) {
+  for (int s = 0; s < kStages; ++s) {
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) issue(s, k);
     advance();
   }
-  __builtin_amdgcn_s_waitcnt(wait_vm((kONS - 1) * kLoads));
+  __builtin_amdgcn_s_waitcnt(wait_vm((kStages - 1) * kLoads));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   Frag f0, f1;
@@ -322,7 +421,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     auto stage = [&](auto own_tag) __attribute__((always_inline)) {
       constexpr int own = decltype(own_tag)::value;   // row block whose rows the stage holds, or -1
       const int b0 = ring;
-      const int b1 = (ring + 1) & (kONS - 1);
+      const int b1 = (ring + 1) & (kStages - 1);
       step(f0, [&](int k) __attribute__((always_inline)) {
         if (k % kEvery == 0) read_op(b0, 1, k / kEvery, f1);
       });
@@ -387,7 +486,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
           }
       }
     };
-    // before the tile's last kONS stages, which load the next tile's first ones
+    // before the tile's last kStages stages, which load the next tile's first ones
     // (behind the last tile: this tile's again, never used, so that every wait
     // counts the same)
     const int tn = tile_at(round + 1);
@@ -400,16 +499,16 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     };
     using None = std::integral_constant<int, -1>;
     if constexpr (kSym) {
-      for (int x = kONS; x < nkb; ++x) stage(None{});
+      for (int x = kStages; x < nkb; ++x) stage(None{});
       turn();
 #pragma unroll 1
-      for (int x = 0; x < kONS; ++x) stage(None{});
+      for (int x = 0; x < kStages; ++x) stage(None{});
     } else {
       // the stages of the wave's own row blocks apart (no branch may hold
       // MFMAs: the accumulators would leave their registers)
       int x = 0;
       auto one = [&](auto own_tag) __attribute__((always_inline)) {
-        if (x == nkb - kONS) turn();
+        if (x == nkb - kStages) turn();
         stage(own_tag);
         ++x;
       };
@@ -424,9 +523,8 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
 
     // ---- epilogue
     const OrthJob& jb = g.job;
-    unsigned char* stg = smem + kONS * kStage + wave * 4096;
-    typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
-    u16x8 ob[2][2];                                 // kFinal: the two blocks of a 64-element piece of rows
+    unsigned char* stg = smem + kStages * kStage + wave * 4096;
+    u32x4 ob[2][2];                                 // kFinal: the two blocks of a 64-element piece of rows
 #pragma unroll
     for (int q = 0; q < kBlocks; ++q) {
       const int i = MODE == kFinal ? q / WB : q % WB, j = MODE == kFinal ? q % WB : q / WB;
@@ -440,74 +538,38 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
         const bool diag = kSym && rb == cb;
         // 8 consecutive columns a lane: 16 p + 8 h + 0..7
         float v[2][8];
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[8 * p + e]),
-                                                             __float_as_uint(c[8 * p + 4 + e]), false, false);
-            v[p][e] = __uint_as_float(sw[0]);
-            v[p][4 + e] = __uint_as_float(sw[1]);
-          }
         const float dpi = dp[bi];
         const Ahead& pe = pre[q % kAhead];
-        f16x8 w[2], wl[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          if constexpr (MODE == kGram) {
-            const float f = jb.so / (jb.sp * jb.sq);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[p][e] *= f;
-          } else if constexpr (MODE == kPoly) {
-            // c R^2 + b R: c (R R + (d_i + d_j) R_ij) + b R_ij off the diagonal
-            const float f = kC * jb.so / (jb.sp * jb.sq), f1 = jb.so / jb.sq;
-            const float u = fmaf(kC * f1, dpi, kB * f1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[p][e] = fmaf(static_cast<float>(pe.a[p][e]), fmaf(kC * f1, dq[bj & 1][8 * p + e], u), v[p][e] * f);
-          } else if constexpr (MODE == kMul) {
-            const float f = jb.so / (jb.sp * jb.sq), fp = jb.so / jb.sp, u = dpi * (jb.so / jb.sq);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[p][e] = fmaf(static_cast<float>(pe.b[p][e]), dq[bj & 1][8 * p + e] * fp,
-                             fmaf(static_cast<float>(pe.a[p][e]), u, v[p][e] * f));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float y = fmaf(static_cast<float>(pe.a[p][e]), dpi, v[p][e] * (1.0f / kSQ));
-              v[p][e] = y;
-              if constexpr (MODE == kApply) {
-                w[p][e] = static_cast<_Float16>(y);
-                wl[p][e] = static_cast<_Float16>(y - static_cast<float>(w[p][e]));
-              }
-            }
-          }
+          const float half[8] = {c[8 * p],     c[8 * p + 1], c[8 * p + 2], c[8 * p + 3],
+                                 c[8 * p + 4], c[8 * p + 5], c[8 * p + 6], c[8 * p + 7]};
+          gather_columns(half, v[p]);
+          finish<MODE>(v[p], pe.a[p], pe.b[MODE == kMul ? p : 0], dpi,
+                       dq[MODE == kPoly || MODE == kMul ? bj & 1 : 0] + 8 * p, jb);
         }
         if (q + kAhead < kBlocks) fetch(q + kAhead);
+        f16x8 w[2], wl[2];
         if constexpr (kSym) {
           if (diag) {
-            // split into e, exact in fp16, and what is left of it
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
               const int at = r - 16 * p - 8 * h;    // this lane's diagonal element
               if (at >= 0 && at < 8) {
-                float d = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d = e == at ? v[p][e] : d;
-                if constexpr (MODE == kPoly) d = fmaf(jb.so, fmaf(dpi, fmaf(kC, dpi, kB), kA), d);
-                if constexpr (MODE == kMul) d = fmaf(jb.so * dpi, jb.dq[static_cast<size_t>(cur.mat) * g.d_stride +
-                                                                       32 * min(cb, g.nb - 1) + r], d);
-                const float e16 = static_cast<float>(static_cast<_Float16>(d));
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[p][e] = e == at ? d - e16 : v[p][e];
-                if (inside) jb.dout[static_cast<size_t>(cur.mat) * g.d_stride + 32 * rb + r] = e16 / jb.so;
+                const float dqi = MODE == kMul ? jb.dq[static_cast<size_t>(cur.mat) * g.d_stride +
+                                                       32 * min(cb, g.nb - 1) + r] : 0.0f;
+                const float d = split_diagonal<MODE>(v[p], at, dpi, dqi, jb.so);
+                if (inside) jb.dout[static_cast<size_t>(cur.mat) * g.d_stride + 32 * rb + r] = d;
               }
             }
           }
+        }
+        if constexpr (MODE != kFinal) {
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[p][e] = static_cast<_Float16>(v[p][e]);
+          for (int p = 0; p < 2; ++p) {
+            w[p] = to_f16(v[p]);
+            if constexpr (MODE == kApply) wl[p] = low_part(v[p], w[p]);
+          }
         }
         if constexpr (MODE != kFinal) {
           if (inside) {
@@ -528,11 +590,8 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
             }
           }
         } else {
-          const float f = g.scale / kSX;
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ob[q & 1][p][e] = f32_to_bf16(v[p][e] * f);
+          for (int p = 0; p < 2; ++p) ob[q & 1][p] = to_bf16(v[p], g.scale / kSX);
         }
       };
       if constexpr (MODE != kFinal) {
@@ -552,39 +611,27 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
             // lane: row 32 cb + r of the caller's matrix, 8 of its columns
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              *reinterpret_cast<u16x8*>(stg + 2048 * t + run0) = ob[t][0];
-              *reinterpret_cast<u16x8*>(stg + 2048 * t + 1024 + run1) = ob[t][1];
+              *reinterpret_cast<u32x4*>(stg + 2048 * t + run0) = ob[t][0];
+              *reinterpret_cast<u32x4*>(stg + 2048 * t + 1024 + run1) = ob[t][1];
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int p = 0; p < 2; ++p) ob[t][p] = __builtin_bit_cast(u16x8, tr_run(stg + 2048 * t, p, lane));
+              for (int p = 0; p < 2; ++p) ob[t][p] = __builtin_bit_cast(u32x4, tr_run(stg + 2048 * t, p, lane));
           }
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-              *reinterpret_cast<u16x8*>(stg + r * 128 + (((4 * t + 2 * p + h) ^ ((r >> 1) & 7)) << 4)) = ob[t][p];
+              *reinterpret_cast<u32x4*>(stg + r * 128 + (((4 * t + 2 * p + h) ^ ((r >> 1) & 7)) << 4)) = ob[t][p];
           // first caller row and column of the piece
           const int ur0 = 32 * (g.tall ? col_block(i) : row_block(i));
           const int uc0 = 32 * (g.tall ? row_block(j - 1) : col_block(j - 1));
-          bf16_t* user = g.user + static_cast<size_t>(cur.mat) * g.rows * g.cols;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int row = 8 * k + (lane >> 3), ch = lane & 7;
             const u32x4 x = *reinterpret_cast<const u32x4*>(stg + row * 128 + ((ch ^ ((row >> 1) & 7)) << 4));
-            const int ur = ur0 + row, uc = uc0 + 8 * ch;
-            if (ur < g.rows && uc < g.cols) {
-              bf16_t* dst = user + static_cast<size_t>(ur) * g.cols + uc;
-              typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
-              if (uc + 8 <= g.cols) {
-                *reinterpret_cast<u32x4u*>(dst) = x;
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (uc + e < g.cols) dst[e] = static_cast<bf16_t>(x[e >> 1] >> (16 * (e & 1)));
-              }
-            }
+            store_user(g, cur.mat, ur0 + row, uc0 + 8 * ch, x);
           }
         }
       }
@@ -596,6 +643,213 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
   }
   // trailing loads land before the workgroup's LDS is given up
   __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+}
+
+// The same products for few tiles, where a tile's latency counts and not the
+// matrix cores' rate: tiles of 64 x 64, a workgroup of 8 waves each, which
+// share out the stages of K.  Operands go from global memory straight into
+// registers in operand order (x's blocks through 4 KB of LDS, for the
+// transposing read), the loads of 2 to 4 stages a wave in flight, no barrier
+// until the waves' sums are joined through LDS in a fixed order.  Wave u then
+// finishes 32 rows x 16 columns, half of block u / 2.
+constexpr int kSThreads = 512;
+constexpr int kSWaves = kSThreads / 64;
+constexpr int kSAhead = 2;             // stages a wave loads at once, two sets in turn
+
+template <int MODE>
+__global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
+  constexpr bool kSym = MODE <= kMul;
+  constexpr bool kTr = !kSym;
+  constexpr int kHalf = kSWaves / 2;
+  // the waves' sums (half of them at a time); before that, x's blocks; behind
+  // it, finished blocks on their way to a transposed store
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kHalf * 16384 + 8192];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, h = lane >> 5;
+  const int mt = (g.mb + 1) / 2, nt = (g.nb + 1) / 2;
+  const int per_mat = kSym ? mt * (mt + 1) / 2 : mt * nt;
+  const int total = per_mat * g.count;
+  // runs of consecutive tiles on the XCDs (workgroup b runs on XCD b mod 8)
+  const int per_xcd = (total + kOXcds - 1) / kOXcds;
+  const int ti = (blockIdx.x % kOXcds) * per_xcd + blockIdx.x / kOXcds;
+  if (ti >= total) return;
+  const int mat = ti / per_mat, l = ti - mat * per_mat;
+  int i0, j0;
+  if constexpr (kSym) {
+    triangle(l, i0, j0);
+  } else {
+    j0 = l / mt;
+    i0 = l - j0 * mt;
+  }
+  // (x's row tiles are all whole, as in the kernel above)
+  const int rb0 = __builtin_amdgcn_readfirstlane(kTr ? min(2 * i0, g.mb - 2) : 2 * i0);
+  const int cb0 = __builtin_amdgcn_readfirstlane(2 * j0);
+  const OrthJob& jb = g.job;
+  const unsigned char* P = reinterpret_cast<const unsigned char*>(jb.p + mat * g.p_stride);
+  const unsigned char* Q = reinterpret_cast<const unsigned char*>(jb.q + mat * g.q_stride);
+  const size_t row_bytes = static_cast<size_t>(g.K) * 64;      // a row block of a row-operand matrix
+  const int nkb = g.K / kOBK;
+  const int run[2] = {run_off(r, h, 0), run_off(r, h, 1)};
+  const float* dpm = MODE == kGram ? nullptr : jb.dp + static_cast<size_t>(mat) * g.d_stride;
+
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{0.f};
+  unsigned char* mine = smem + wave * 4096;
+  struct Set {
+    f16x8 p[kSAhead][2][2], q[kSAhead][2][2];
+  };
+  auto load = [&](int base, Set& t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < kSAhead; ++s) {
+      // (a stage past the end loads the last one again: in bounds, not used)
+      const int kb = min(base + s * kSWaves, nkb - 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const unsigned char* ps = P + min(rb0 + i, g.mb - 1) * row_bytes + kb * 2048;
+        const int cb = min(cb0 + i, g.nb - 1);
+        const unsigned char* qs = kTr ? Q + (static_cast<size_t>(kb) * g.nb + cb) * 2048 : Q + cb * row_bytes + kb * 2048;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          t.p[s][i][o] = *reinterpret_cast<const f16x8*>(ps + o * 1024 + run[o]);
+          t.q[s][i][o] = *reinterpret_cast<const f16x8*>(qs + o * 1024 + (kTr ? lane * 16 : run[o]));
+        }
+      }
+    }
+  };
+  auto use = [&](int base, Set& t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < kSAhead; ++s) {
+      const int kb = base + s * kSWaves;
+      if (kb < nkb) {
+        if constexpr (kTr) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+              *reinterpret_cast<f16x8*>(mine + j * 2048 + o * 1024 + lane * 16) = t.q[s][j][o];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int st = 0; st < 2; ++st) t.q[s][j][st] = tr_run(mine + j * 2048, st, lane);
+        }
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (kTr) {
+              // the diagonal's part: diag(e) times x's own rows
+              if (kb == rb0 + i) {
+                const float e16 = dpm[32 * (rb0 + i) + r] * kSQ;
+                const int at = r - 16 * st - 8 * h;
+                f16x8 e;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e[k] = k == at ? static_cast<_Float16>(e16) : static_cast<_Float16>(0.0f);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(t.q[s][j][st], e, acc[i][j], 0, 0, 0);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(t.q[s][j][st], t.p[s][i][st], acc[i][j], 0, 0, 0);
+          }
+      }
+    }
+  };
+  constexpr int kStep = kSWaves * kSAhead;
+  Set s0, s1;
+  load(wave, s0);
+  for (int base = wave; base < nkb; base += 2 * kStep) {
+    if (base + kStep < nkb) load(base + kStep, s1);
+    use(base, s0);
+    if (base + 2 * kStep < nkb) load(base + 2 * kStep, s0);
+    use(base + kStep, s1);
+  }
+
+  // ---- this wave's part of the output: rows of row block i, columns 16 p .. of column block j
+  const int unit = wave >> 1, p = wave & 1, ui = unit >> 1, uj = unit & 1;
+  const int rb = rb0 + ui, cb = cb0 + uj;
+  const bool inside = rb < g.mb && cb < g.nb;
+  const size_t o16 = static_cast<size_t>(2 * g.nb);
+  const size_t blk = ((static_cast<size_t>(min(rb, g.mb - 1)) * o16 + 2 * min(cb, g.nb - 1) + p) * 1024 + run[p]) / 2;
+  f16x8 ea{}, eb{};
+  float dpi = 0.0f, dq[8] = {}, dqi = 0.0f;
+  if constexpr (MODE != kGram) {
+    ea = *reinterpret_cast<const f16x8*>((kSym ? jb.q : jb.lo) + mat * g.q_stride + blk);
+    if constexpr (MODE == kMul) eb = *reinterpret_cast<const f16x8*>(jb.p + mat * g.p_stride + blk);
+    dpi = dpm[32 * min(rb, g.mb - 1) + r];
+  }
+  if constexpr (MODE == kPoly || MODE == kMul) {
+    const float* d = jb.dq + static_cast<size_t>(mat) * g.d_stride + 32 * min(cb, g.nb - 1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dq[e] = d[16 * p + 8 * h + e];
+    dqi = d[r];
+  }
+  float* red = reinterpret_cast<float*>(smem);
+  __syncthreads();                                    // x's blocks have been read
+  auto exchange = [&](bool store, int slot) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float* at = red + (slot * 64 + b * 16 + k) * 64 + lane;
+        if (store) *at = acc[b >> 1][b & 1][k];
+        else acc[b >> 1][b & 1][k] += *at;
+      }
+  };
+  if (wave >= kHalf) exchange(true, wave - kHalf);
+  __syncthreads();
+  if (wave < kHalf) {
+    exchange(false, wave);
+    exchange(true, wave);
+  }
+  __syncthreads();
+  float c[8], v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    c[k] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kHalf; ++w) c[k] += red[(w * 64 + unit * 16 + 8 * p + k) * 64 + lane];
+  }
+  gather_columns(c, v);
+  finish<MODE>(v, ea, eb, dpi, dq, jb);
+  if constexpr (kSym) {
+    const int at = r - 16 * p - 8 * h;
+    if (rb == cb && at >= 0 && at < 8) {
+      const float d = split_diagonal<MODE>(v, at, dpi, dqi, jb.so);
+      if (inside) jb.dout[static_cast<size_t>(mat) * g.d_stride + 32 * rb + r] = d;
+    }
+  }
+  unsigned char* flip = smem + kHalf * 16384 + unit * 2048;
+  if constexpr (MODE != kFinal) {
+    const f16x8 w = to_f16(v);
+    if (inside) {
+      *reinterpret_cast<f16x8*>(jb.out + mat * g.out_stride + blk) = w;
+      if constexpr (MODE == kApply) *reinterpret_cast<f16x8*>(jb.out_lo + mat * g.out_stride + blk) = low_part(v, w);
+    }
+    if constexpr (kSym) {
+      if (rb0 != cb0) {                               // the mirror image
+        *reinterpret_cast<f16x8*>(flip + p * 1024 + run[p]) = w;
+        __syncthreads();
+        const f16x8 t = tr_run(flip, p, lane);
+        if (inside)
+          *reinterpret_cast<f16x8*>(jb.out + mat * g.out_stride +
+                                    ((static_cast<size_t>(cb) * o16 + 2 * rb + p) * 1024 + run[p]) / 2) = t;
+      }
+    }
+  } else {
+    u32x4 o = to_bf16(v, g.scale / kSX);
+    if (g.tall) {
+      *reinterpret_cast<u32x4*>(flip + p * 1024 + run[p]) = o;
+      __syncthreads();
+      o = __builtin_bit_cast(u32x4, tr_run(flip, p, lane));
+    }
+    store_user(g, mat, 32 * (g.tall ? cb : rb) + r, 32 * (g.tall ? rb : cb) + 16 * p + 8 * h, o);
+  }
 }
 
 // ------------------------------------------------------------------ input
@@ -635,6 +889,13 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
       for (int e = 0; e < 4; ++e) v[4 * k + e] = __uint_as_float(w[e]);
     }
   }
+}
+
+// What u is multiplied by, in x's stored scale, from its sum of squares: an
+// infinity or a NaN anywhere makes the whole matrix NaN, a zero matrix stays 0.
+__device__ __forceinline__ double inverse_norm(double s, float eps) {
+  const double norm = sqrt(s) + static_cast<double>(eps);
+  return s < 1.0 / 0.0 ? (norm > 0.0 ? kSX / norm : 0.0) : 0.0 / 0.0;
 }
 
 // Sums of squares of the update u = g (or, with momentum, M <- mu M + g and
@@ -733,11 +994,7 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
     for (int i = tid; i < parts; i += 64) s += sums[static_cast<size_t>(mat) * parts + i];
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-    if (tid == 0) {
-      const double norm = sqrt(s) + static_cast<double>(eps);
-      // an infinity or a NaN anywhere makes the whole matrix NaN
-      s_inv = s < 1.0 / 0.0 ? (norm > 0.0 ? kSX / norm : 0.0) : 0.0 / 0.0;
-    }
+    if (tid == 0) s_inv = inverse_norm(s, eps);
   }
   __syncthreads();
   const double inv = s_inv;
@@ -772,6 +1029,405 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
     *reinterpret_cast<u32x4*>(hi + at + i * 8) = *reinterpret_cast<const u32x4*>(buf[0] + i * 16);
     *reinterpret_cast<u32x4*>(lo + at + i * 8) = *reinterpret_cast<const u32x4*>(buf[1] + i * 16);
   }
+}
+
+// ------------------------------------------------------------ small matrices
+// A whole update in one workgroup, for matrices whose x fits its LDS: the
+// launches of the general path (16 of about 5 us) would be most of the time.
+//   * x stays in registers, in fp32 and in accumulator order: wave w owns the
+//     blocks w, w + 8, ... (row block t mod MB, column block t / MB); its fp16
+//     copy, the products' operand, is in LDS in blocks as above;
+//   * the symmetric matrix, R and then in its place Q, is in LDS with zeros on
+//     the diagonal and the diagonal in fp32 beside it;
+//   * a step: R's lower blocks dealt to the waves (for few blocks also K, the
+//     parts joined through LDS in order), Q's likewise, then every wave its
+//     blocks of Q x; the block's elementwise part d_i x_ij is in fp32.
+constexpr int kResMaxMB = 6;
+constexpr int kResBlocks = 8;                         // blocks of x a wave owns at most
+constexpr int kResLoads = 4;                          // blocks whose input is loaded at once
+constexpr int kResLds = 160 * 1024;
+
+// column blocks of x that fit beside the rest
+constexpr int res_split(int mb) { return mb == 1 ? 4 : mb == 2 ? 2 : 1; }
+constexpr int res_fixed(int mb) {
+  return mb * mb * 2048 + (res_split(mb) - 1) * (mb * (mb + 1) / 2) * 4096 + 2 * mb * 32 * 4 + 256;
+}
+constexpr int res_cols(int mb) {
+  const int lds = (kResLds - res_fixed(mb)) / (mb * 2048), regs = kResBlocks * 8 / mb;
+  return lds < regs ? lds : regs;
+}
+
+// A uniform value the compiler knows nothing about: what is computed from it
+// stays where it is used (hoisted out of the steps, the addresses of every
+// block would take the registers of x).
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+template <typename T, int MB>
+__global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, float* mom, float mu, bool nesterov,
+                                                                  int rows, int cols, bool tall, int nb, int steps,
+                                                                  float eps, float scale, bf16_t* out) {
+  constexpr int kTri = MB * (MB + 1) / 2, kSplit = res_split(MB), kItems = kTri * kSplit;
+  constexpr int kMine = (kItems + kSWaves - 1) / kSWaves;      // blocks of R a wave computes
+  constexpr int kQMine = (kTri + kSWaves - 1) / kSWaves;       // blocks of Q
+  constexpr int kXBytes = MB * res_cols(MB) * 2048;
+  constexpr int kStageBytes = 32 * 33 * 4;                     // a block in fp32, rows padded
+  static_assert(kXBytes >= kSWaves * kStageBytes, "the waves' staging blocks share x's place");
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kXBytes + res_fixed(MB)];
+  unsigned char* xs = smem;
+  unsigned char* ms = smem + kXBytes;                          // R, then Q
+  float* part = reinterpret_cast<float*>(ms + MB * MB * 2048);
+  float* rd = part + (kSplit - 1) * kTri * 1024;
+  float* qd = rd + 32 * MB;
+  double* red = reinterpret_cast<double*>(qd + 32 * MB);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 31, h = lane >> 5;
+  const int run[2] = {run_off(r, h, 0), run_off(r, h, 1)};
+  const int mat = blockIdx.x;
+  const size_t base = static_cast<size_t>(mat) * rows * cols;
+  const int blocks = MB * nb;
+  float* stg = reinterpret_cast<float*>(xs + wave * kStageBytes);
+
+  // ---- the update u, block by block: whole pieces of the caller's rows into
+  // the wave's staging block, from there in accumulator order
+  float x[kResBlocks][16];
+  double ss = 0.0;
+#pragma unroll
+  for (int t0 = 0; t0 < kResBlocks; t0 += kResLoads) {
+    float v[kResLoads][2][8], m[kResLoads][2][8];
+    // half k of block t: 8 elements from (row, col) of the caller's matrix
+    auto place = [&](int t, int k, int& ur, int& uc) __attribute__((always_inline)) {
+      const int b = opaque(wave + kSWaves * t);
+      ur = 32 * (tall ? b / MB : b % MB) + 16 * k + (lane >> 2);
+      uc = 32 * (tall ? b % MB : b / MB) + 8 * (lane & 3);
+      return b < blocks && ur < rows && uc < cols;
+    };
+#pragma unroll
+    for (int s = 0; s < kResLoads; ++s)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        int ur, uc;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[s][k][e] = m[s][k][e] = 0.0f;
+        if (place(t0 + s, k, ur, uc)) {
+          const size_t at = base + static_cast<size_t>(ur) * cols + uc;
+          if (uc + 8 <= cols) {
+            load8(gp + at, v[s][k]);
+            if (mom != nullptr) load8(mom + at, m[s][k]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (uc + e < cols) {
+                v[s][k][e] = load_elem(gp + at + e);
+                if (mom != nullptr) m[s][k][e] = mom[at + e];
+              }
+          }
+        }
+      }
+#pragma unroll
+    for (int s = 0; s < kResLoads; ++s) {
+      const int t = t0 + s;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        int ur, uc;
+        const bool in = place(t, k, ur, uc);
+        if (mom != nullptr) {
+          // (elements past the row's end are 0 and stay 0)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            m[s][k][e] = fmaf(mu, m[s][k][e], v[s][k][e]);
+            v[s][k][e] = nesterov ? fmaf(mu, m[s][k][e], v[s][k][e]) : m[s][k][e];
+          }
+          if (in) {
+            const size_t at = base + static_cast<size_t>(ur) * cols + uc;
+            if (uc + 8 <= cols) {
+              store_f32x8(mom + at, m[s][k]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (uc + e < cols) mom[at + e] = m[s][k][e];
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) stg[(16 * k + (lane >> 2)) * 33 + 8 * (lane & 3) + e] = v[s][k][e];
+      }
+      // register q of a lane: row r, column 8 (q / 4) + 4 h + q mod 4 (blocks
+      // past the matrix are zeros)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int c = 8 * (q >> 2) + 4 * h + (q & 3);
+        x[t][q] = tall ? stg[c * 33 + r] : stg[r * 33 + c];
+        ss = fma(static_cast<double>(x[t][q]), static_cast<double>(x[t][q]), ss);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) ss += __shfl_xor(ss, d);
+  if (lane == 0) red[wave] = ss;
+  __syncthreads();
+  ss = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSWaves; ++w) ss += red[w];
+  const double inv = inverse_norm(ss, eps);
+#pragma unroll
+  for (int t = 0; t < kResBlocks; ++t) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      asm volatile("" : "+v"(x[t][q]));               // (or the conversions to 64 bits above would be kept)
+      x[t][q] = static_cast<float>(x[t][q] * inv);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  auto columns = [&](const float (&c)[16], int p, float (&v)[8]) __attribute__((always_inline)) {
+    float half[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) half[e] = c[8 * p + e];
+    gather_columns(half, v);
+  };
+  auto put_x = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < kResBlocks; ++t) {
+      const int b = opaque(wave + kSWaves * t);
+      if (b < blocks) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float v[8];
+          columns(x[t], p, v);
+          *reinterpret_cast<f16x8*>(xs + ((b % MB) * 2 * nb + 2 * (b / MB) + p) * 1024 + run[p]) = to_f16(v);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // a lower block (i, j) of the symmetric matrix and its mirror image
+  auto put_sym = [&](int i, int j, const f16x8 (&w)[2]) __attribute__((always_inline)) {
+    unsigned char* at = ms + (i * 2 * MB + 2 * j) * 1024;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *reinterpret_cast<f16x8*>(at + p * 1024 + run[p]) = w[p];
+    if (i != j) {
+      const f16x8 t[2] = {tr_run(at, 0, lane), tr_run(at, 1, lane)};
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        *reinterpret_cast<f16x8*>(ms + (j * 2 * MB + 2 * i + p) * 1024 + run[p]) = t[p];
+    }
+  };
+
+  // the blocks of R and of Q this wave computes
+  int gi[kMine], gj[kMine], qi[kQMine], qj[kQMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    int i, j;
+    triangle((wave + kSWaves * k) / kSplit, i, j);
+    gi[k] = __builtin_amdgcn_readfirstlane(i);
+    gj[k] = __builtin_amdgcn_readfirstlane(j);
+  }
+#pragma unroll
+  for (int k = 0; k < kQMine; ++k) {
+    int i, j;
+    triangle(wave + kSWaves * k, i, j);
+    qi[k] = __builtin_amdgcn_readfirstlane(i);
+    qj[k] = __builtin_amdgcn_readfirstlane(j);
+  }
+
+  for (int step = 0; step < steps; ++step) {
+    put_x();
+    __syncthreads();
+    // ---- R = x x^T
+    f32x16 acc[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      acc[k] = f32x16{0.f};
+      const int it = opaque(wave + kSWaves * k);
+      if (it < kItems) {
+        const int i = opaque(gi[k]), j = opaque(gj[k]);
+        const unsigned char* pi = xs + i * 2 * nb * 1024;
+        const unsigned char* pj = xs + j * 2 * nb * 1024;
+        // two stages' operands at a time
+        int kb = it % kSplit;
+        for (; kb + kSplit < nb; kb += 2 * kSplit) {
+          f16x8 a[4], b[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int at = (2 * (kb + kSplit * (z >> 1)) + (z & 1)) * 1024 + run[z & 1];
+            a[z] = *reinterpret_cast<const f16x8*>(pi + at);
+            b[z] = *reinterpret_cast<const f16x8*>(pj + at);
+          }
+#pragma unroll
+          for (int z = 0; z < 4; ++z) acc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[z], a[z], acc[k], 0, 0, 0);
+        }
+        if (kb < nb) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const f16x8 a = *reinterpret_cast<const f16x8*>(pi + (2 * kb + st) * 1024 + run[st]);
+            const f16x8 b = *reinterpret_cast<const f16x8*>(pj + (2 * kb + st) * 1024 + run[st]);
+            acc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, acc[k], 0, 0, 0);
+          }
+        }
+        if (kSplit > 1 && it % kSplit != 0) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            part[(((it % kSplit - 1) * kTri + it / kSplit) * 16 + q) * 64 + lane] = acc[k][q];
+        }
+      }
+    }
+    if constexpr (kSplit > 1) __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int it = opaque(wave + kSWaves * k);
+      if (it < kItems && it % kSplit == 0) {
+        const int i = opaque(gi[k]), j = opaque(gj[k]);
+        float c[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          c[q] = acc[k][q];
+#pragma unroll
+          for (int z = 0; z < kSplit - 1; ++z) c[q] += part[((z * kTri + it / kSplit) * 16 + q) * 64 + lane];
+          c[q] *= 1.0f / kSX;
+        }
+        f16x8 w[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float v[8];
+          columns(c, p, v);
+          const int at = r - 16 * p - 8 * h;
+          if (i == j && at >= 0 && at < 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e == at) {
+                rd[32 * i + r] = v[e] * (1.0f / kSX);
+                v[e] = 0.0f;
+              }
+          }
+          w[p] = to_f16(v);
+        }
+        put_sym(i, j, w);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    // ---- Q = a I + b R + c R^2, kept in registers until R has been read
+    f16x8 qw[kQMine][2];
+#pragma unroll
+    for (int k = 0; k < kQMine; ++k) {
+      const int it = opaque(wave + kSWaves * k);
+      if (it < kTri) {
+        const int i = opaque(qi[k]), j = opaque(qj[k]);
+        f32x16 a2 = f32x16{0.f};
+#pragma unroll
+        for (int kb = 0; kb < 2 * MB; ++kb) {
+          const f16x8 a = *reinterpret_cast<const f16x8*>(ms + (i * 2 * MB + kb) * 1024 + run[kb & 1]);
+          const f16x8 b = *reinterpret_cast<const f16x8*>(ms + (j * 2 * MB + kb) * 1024 + run[kb & 1]);
+          a2 = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, a, a2, 0, 0, 0);
+        }
+        float c[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) c[q] = a2[q];
+        const float di = rd[32 * i + r];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          float v[8];
+          columns(c, p, v);
+          const f16x8 m = *reinterpret_cast<const f16x8*>(ms + (i * 2 * MB + 2 * j + p) * 1024 + run[p]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float dj = rd[32 * j + 16 * p + 8 * h + e];
+            v[e] = fmaf(static_cast<float>(m[e]) * (kSQ / kSX), fmaf(kC, di + dj, kB), v[e] * (kC * kSQ / (kSX * kSX)));
+          }
+          const int at = r - 16 * p - 8 * h;
+          if (i == j && at >= 0 && at < 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e == at) {
+                qd[32 * i + r] = fmaf(v[e], 1.0f / kSQ, fmaf(di, fmaf(kC, di, kB), kA));
+                v[e] = 0.0f;
+              }
+          }
+          qw[k][p] = to_f16(v);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kQMine; ++k) {
+      const int it = opaque(wave + kSWaves * k);
+      if (it < kTri) {
+        const int i = opaque(qi[k]), j = opaque(qj[k]);
+        put_sym(i, j, qw[k]);
+      }
+    }
+    __syncthreads();
+    // ---- x <- Q x
+#pragma unroll
+    for (int t = 0; t < kResBlocks; ++t) {
+      const int b = opaque(wave + kSWaves * t);
+      if (b < blocks) {
+        const int i = b % MB, j = b / MB;
+        f32x16 y = f32x16{0.f};
+#pragma unroll
+        for (int kb = 0; kb < MB; ++kb)
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const f16x8 a = *reinterpret_cast<const f16x8*>(ms + (i * 2 * MB + 2 * kb + st) * 1024 + run[st]);
+            y = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_run(xs + (kb * 2 * nb + 2 * j) * 1024, st, lane), a, y, 0, 0, 0);
+          }
+        const float di = qd[32 * i + r];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) x[t][q] = fmaf(di, x[t][q], y[q] * (1.0f / kSQ));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();                                           // x's copy has been read
+  }
+
+  // ---- out, through the staging blocks
+#pragma unroll
+  for (int t = 0; t < kResBlocks; ++t) {
+    const int b = opaque(wave + kSWaves * t);
+    if (b < blocks) {
+      const int ib = b % MB, jb = b / MB;
+      const int ur0 = 32 * (tall ? jb : ib), uc0 = 32 * (tall ? ib : jb);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int c = 8 * (q >> 2) + 4 * h + (q & 3);
+        stg[tall ? c * 33 + r : r * 33 + c] = x[t][q];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = 16 * k + (lane >> 2), col = 8 * (lane & 3);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = stg[row * 33 + col + e];
+        store_rows(out + base, rows, cols, ur0 + row, uc0 + col, to_bf16(v, scale / kSX));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <typename T, int MB>
+void launch_resident(int64_t count, int rows, int cols, const T* g, float* mom, float mu, bool nesterov, int steps,
+                     float eps, float scale, bf16_t* out, hipStream_t st) {
+  const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  if constexpr (MB > 1) {
+    if ((m + 31) / 32 < MB)
+      return launch_resident<T, MB - 1>(count, rows, cols, g, mom, mu, nesterov, steps, eps, scale, out, st);
+  }
+  orth_resident_kernel<T, MB><<<static_cast<int>(count), kSThreads, 0, st>>>(
+      g, mom, mu, nesterov, rows, cols, rows > cols, (n + 31) / 32, steps, eps, scale, out);
+}
+
+bool resident(int m, int n) {
+  const int mb = (m + 31) / 32, nb = (n + 31) / 32;
+  constexpr int most[kResMaxMB] = {res_cols(1), res_cols(2), res_cols(3), res_cols(4), res_cols(5), res_cols(6)};
+  return mb <= kResMaxMB && nb <= most[mb - 1];
 }
 
 // -------------------------------------------------------------- workspace
@@ -822,20 +1478,45 @@ void launch_one(const OrthArgs& a, hipStream_t st) {
 
 template <int MODE>
 void launch_mode(const OrthArgs& a, hipStream_t st) {
-  const int mt = (a.mb + 7) / 8, nt = (a.nb + 7) / 8;
-  const int64_t tiles = static_cast<int64_t>(MODE <= kMul ? mt * (mt + 1) / 2 : mt * nt) * a.count;
-  if (tiles >= 192 && a.mb >= 8) launch_one<4, MODE>(a, st);
-  else launch_one<2, MODE>(a, st);
+  auto tiles_of = [&](int blocks) {
+    const int64_t mt = (a.mb + blocks - 1) / blocks, nt = (a.nb + blocks - 1) / blocks;
+    return (MODE <= kMul ? mt * (mt + 1) / 2 : mt * nt) * a.count;
+  };
+  // One round of 64-wide tiles where they fit one (update of 1 matrix of
+  // 256 x 2048: 122 us against 143 with 128-wide ones); 256-wide tiles where
+  // there are enough of them and K pays for their long epilogue (256 matrices
+  // of 1024 x 2048: 12.1 ms against 14.5; 32 of 512 x 2048, K = 512: products
+  // with x 82 us against 72 with 128-wide ones).
+  if (tiles_of(2) <= 256) {
+    const int64_t tiles = tiles_of(2);
+    orth_small_kernel<MODE><<<static_cast<int>((tiles + 7) / 8 * 8), kSThreads, 0, st>>>(a);
+  } else if (tiles_of(8) >= 192 && a.mb >= 8 && (MODE <= kMul || a.K >= 1024)) {
+    launch_one<4, MODE>(a, st);
+  } else {
+    launch_one<2, MODE>(a, st);
+  }
 }
 
 }  // namespace
 
-size_t orth_workspace_bytes(int64_t count, int rows, int cols) { return plan_of(count, rows, cols).bytes; }
+size_t orth_workspace_bytes(int64_t count, int rows, int cols) {
+  const OrthPlan p = plan_of(count, rows, cols);
+  return resident(p.m, p.n) ? 256 : p.bytes;
+}
 
 hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, const void* g, float* mom, float mu,
                                 bool nesterov, int steps, float eps, float scale, bf16_t* out, void* workspace,
                                 hipStream_t st) {
   const OrthPlan p = plan_of(count, rows, cols);
+  if (resident(p.m, p.n)) {
+    if (bf16)
+      launch_resident<bf16_t, kResMaxMB>(count, rows, cols, static_cast<const bf16_t*>(g), mom, mu, nesterov, steps,
+                                         eps, scale, out, st);
+    else
+      launch_resident<float, kResMaxMB>(count, rows, cols, static_cast<const float*>(g), mom, mu, nesterov, steps,
+                                        eps, scale, out, st);
+    return hipGetLastError();
+  }
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   _Float16* X[4];
   _Float16* S[4];

@@ -151,6 +151,8 @@ def _orth(L, count=2, rows=64, cols=96, dtype=1, g=P(1), mom=None, mu=0.95, nest
     (dict(count=-1), binding.MOE_ERR_INVALID_ARG, b"negative"),
     (dict(rows=-1), binding.MOE_ERR_INVALID_ARG, b"negative"),
     (dict(count=65536), binding.MOE_ERR_UNSUPPORTED, b"count"),
+    (dict(rows=65537, cols=8), binding.MOE_ERR_UNSUPPORTED, b"65536"),
+    (dict(rows=8, cols=65537), binding.MOE_ERR_UNSUPPORTED, b"65536"),
     (dict(rows=1 << 15, cols=1 << 15), binding.MOE_ERR_UNSUPPORTED, b"2^30"),
     (dict(count=65535, rows=1024, cols=1025), binding.MOE_ERR_UNSUPPORTED, b"2^36"),
     (dict(dtype=3), binding.MOE_ERR_INVALID_ARG, b"dtype"),
