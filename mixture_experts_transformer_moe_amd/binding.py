@@ -163,8 +163,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (2.7 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -639,19 +645,27 @@ def _elem(t: torch.Tensor, what: str) -> int:
     raise ValueError(f"{what} is {t.dtype}: float32 or bfloat16 is wanted")
 
 
-def _expect(t: Optional[torch.Tensor], shape, dtype, device, what: str) -> None:
-    """These entry points take their sizes from a tensor, so the others' are checked here."""
+def _arg(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Optional[int]:
+    """Address of an argument whose sizes the call takes from another tensor (on
+    CUDA device `device`), or None."""
     if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}: "
-                         f"{tuple(shape)} {dtype} on {device} is wanted")
+                         f"{tuple(shape)} {dtype} on the device of the others is wanted")
+    return _ptr(t)
+
+
+def _workspace_arg(t: Optional[torch.Tensor], device: int) -> Optional[int]:
+    if t is not None and t.get_device() != device:
+        raise ValueError(f"workspace is on {t.device}: the device of the other tensors is wanted")
+    return _ptr(t)
 
 
 def _stream_of(stream, t: torch.Tensor) -> int:
     """The given stream, or the current one of the tensors' device, which has to be the current device
     (the library launches on the current device)."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"tensors on {t.device} while cuda:{torch.cuda.current_device()} is current")
     return _stream(stream)
 
@@ -664,13 +678,13 @@ def moe_norm_forward(kind, x, residual, gamma, beta, eps, sum, y, mean, rstd, st
     """Pre-norm of the rows of x [rows, cols] (+ residual)."""
     if x.dim() != 2:
         raise ValueError("x must be [rows, cols]")
-    rows, cols = x.shape
-    for t, what in ((residual, "residual"), (sum, "sum"), (y, "y")):
-        _expect(t, (rows, cols), x.dtype, x.device, what)
-    for t, n, what in ((gamma, cols, "gamma"), (beta, cols, "beta"), (mean, rows, "mean"), (rstd, rows, "rstd")):
-        _expect(t, (n,), torch.float32, x.device, what)
-    _check(lib().moe_norm_forward(int(kind), rows, cols, _elem(x, "x"), _ptr(x), _ptr(residual), _ptr(gamma),
-                                  _ptr(beta), float(eps), _ptr(sum), _ptr(y), _ptr(mean), _ptr(rstd),
+    shape, dt, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
+    rows, cols = shape
+    res, out_sum = _arg(residual, shape, dt, dev, "residual"), _arg(sum, shape, dt, dev, "sum")
+    ga, be = _arg(gamma, (cols,), f32, dev, "gamma"), _arg(beta, (cols,), f32, dev, "beta")
+    out_y = _arg(y, shape, dt, dev, "y")
+    me, rs = _arg(mean, (rows,), f32, dev, "mean"), _arg(rstd, (rows,), f32, dev, "rstd")
+    _check(lib().moe_norm_forward(kind, rows, cols, _elem(x, "x"), _ptr(x), res, ga, be, eps, out_sum, out_y, me, rs,
                                   _stream_of(stream, x)), "moe_norm_forward")
 
 
@@ -678,15 +692,14 @@ def moe_norm_backward(kind, dy, x, gamma, mean, rstd, dsum, dx, dgamma, dbeta, w
     """Gradients of the pre-norm; x is what was normalised (the forward's sum where it had a residual)."""
     if x.dim() != 2:
         raise ValueError("x must be [rows, cols]")
-    rows, cols = x.shape
-    for t, what in ((dy, "dy"), (dsum, "dsum"), (dx, "dx")):
-        _expect(t, (rows, cols), x.dtype, x.device, what)
-    for t, n, what in ((gamma, cols, "gamma"), (mean, rows, "mean"), (rstd, rows, "rstd"), (dgamma, cols, "dgamma"),
-                       (dbeta, cols, "dbeta")):
-        _expect(t, (n,), torch.float32, x.device, what)
-    _check(lib().moe_norm_backward(int(kind), rows, cols, _elem(x, "x"), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean),
-                                   _ptr(rstd), _ptr(dsum), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
-                                   _nbytes(workspace), _stream_of(stream, x)), "moe_norm_backward")
+    shape, dt, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
+    rows, cols = shape
+    _check(lib().moe_norm_backward(
+        kind, rows, cols, _elem(x, "x"), _arg(dy, shape, dt, dev, "dy"), _ptr(x),
+        _arg(gamma, (cols,), f32, dev, "gamma"), _arg(mean, (rows,), f32, dev, "mean"),
+        _arg(rstd, (rows,), f32, dev, "rstd"), _arg(dsum, shape, dt, dev, "dsum"), _arg(dx, shape, dt, dev, "dx"),
+        _arg(dgamma, (cols,), f32, dev, "dgamma"), _arg(dbeta, (cols,), f32, dev, "dbeta"),
+        _workspace_arg(workspace, dev), _nbytes(workspace), _stream_of(stream, x)), "moe_norm_backward")
 
 
 def moe_orthogonalize_workspace_bytes(count, rows, cols) -> int:
@@ -698,10 +711,10 @@ def moe_orthogonalize(g, momentum, mu, nesterov, steps, eps, scale, out, workspa
     (fp32, updated in place) where there is one."""
     if g.dim() not in (2, 3):
         raise ValueError("g must be [rows, cols] or [count, rows, cols]")
-    count = g.shape[0] if g.dim() == 3 else 1
-    rows, cols = g.shape[-2:]
-    _expect(momentum, g.shape, torch.float32, g.device, "momentum")
-    _expect(out, g.shape, torch.bfloat16, g.device, "out")
-    _check(lib().moe_orthogonalize(count, rows, cols, _elem(g, "g"), _ptr(g), _ptr(momentum), float(mu),
-                                   int(bool(nesterov)), int(steps), float(eps), float(scale), _ptr(out),
-                                   _ptr(workspace), _nbytes(workspace), _stream_of(stream, g)), "moe_orthogonalize")
+    shape, dev = g.shape, g.get_device()
+    count = shape[0] if g.dim() == 3 else 1
+    rows, cols = shape[-2:]
+    mo, to = _arg(momentum, shape, torch.float32, dev, "momentum"), _arg(out, shape, torch.bfloat16, dev, "out")
+    _check(lib().moe_orthogonalize(
+        count, rows, cols, _elem(g, "g"), _ptr(g), mo, mu, int(bool(nesterov)), steps, eps, scale, to,
+        _workspace_arg(workspace, dev), _nbytes(workspace), _stream_of(stream, g)), "moe_orthogonalize")

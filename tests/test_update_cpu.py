@@ -168,7 +168,8 @@ def _orth(L, count=2, rows=64, cols=96, dtype=1, g=P(1), mom=None, mu=0.95, nest
     (dict(out=None), binding.MOE_ERR_INVALID_ARG, b"out is NULL"),
     (dict(g=ctypes.c_void_p((1 << 32) + 8)), binding.MOE_ERR_INVALID_ARG, b"aligned"),
     (dict(ws=None), binding.MOE_ERR_WORKSPACE, b"workspace"),
-    (dict(nbytes=1 << 10), binding.MOE_ERR_WORKSPACE, b"workspace"),
+    (dict(nbytes=128), binding.MOE_ERR_WORKSPACE, b"workspace"),
+    (dict(rows=256, cols=1024, nbytes=1 << 20), binding.MOE_ERR_WORKSPACE, b"workspace"),
     (dict(dtype=0, out=P(1)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
     (dict(out=ctypes.c_void_p((1 << 32) + 16)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
     (dict(mom=P(2)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
@@ -194,16 +195,28 @@ def test_orthogonalize_workspace_does_not_depend_on_orientation(L):
 
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     import torch
-    x = torch.zeros(4, 8)
+    x, rms = torch.zeros(4, 8), binding.MOE_NORM_RMS
     with pytest.raises(ValueError, match="device tensors"):
-        binding.moe_norm_forward(binding.MOE_NORM_RMS, x, None, None, None, 1e-6, None, x.clone(), None, None)
-    with pytest.raises(ValueError, match="gamma"):
-        binding.moe_norm_forward(binding.MOE_NORM_RMS, x, None, torch.zeros(7), None, 1e-6, None, x.clone(), None, None)
+        binding.moe_norm_forward(rms, x, None, None, None, 1e-6, None, None, None, None)
+    with pytest.raises(ValueError, match="device tensors"):
+        binding.moe_orthogonalize(x, None, 0.0, True, 5, 1e-7, 1.0, None, None)
+    with pytest.raises(ValueError, match="gamma is"):
+        binding.moe_norm_forward(rms, x, None, torch.zeros(7), None, 1e-6, None, None, None, None)
+    with pytest.raises(ValueError, match="mean is"):
+        binding.moe_norm_forward(rms, x, None, None, None, 1e-6, None, None, torch.zeros(8), None)
     with pytest.raises(ValueError, match="y is"):
-        binding.moe_norm_forward(binding.MOE_NORM_RMS, x, None, None, None, 1e-6, None, torch.zeros(4, 9), None, None)
+        binding.moe_norm_forward(rms, x, None, None, None, 1e-6, None, torch.zeros(4, 9), None, None)
+    with pytest.raises(ValueError, match="rstd is"):
+        binding.moe_norm_forward(rms, x, None, None, None, 1e-6, None, None, None, torch.zeros(4, dtype=torch.float64))
     with pytest.raises(ValueError, match="float32 or bfloat16"):
-        binding.moe_norm_forward(binding.MOE_NORM_RMS, x.half(), None, None, None, 1e-6, None, x.half(), None, None)
+        binding.moe_norm_forward(rms, x.half(), None, None, None, 1e-6, None, None, None, None)
+    with pytest.raises(ValueError, match="dy is"):
+        binding.moe_norm_backward(rms, torch.zeros(4, 7), x, None, None, None, None, None, None, None, None)
     with pytest.raises(ValueError, match="out is"):
         binding.moe_orthogonalize(x, None, 0.0, True, 5, 1e-7, 1.0, x.clone(), None)
+    with pytest.raises(ValueError, match="momentum is"):
+        binding.moe_orthogonalize(x, torch.zeros(8, 4), 0.0, True, 5, 1e-7, 1.0, None, None)
     with pytest.raises(ValueError, match="rows, cols"):
-        binding.moe_orthogonalize(torch.zeros(4), None, 0.0, True, 5, 1e-7, 1.0, torch.zeros(4), None)
+        binding.moe_orthogonalize(torch.zeros(4), None, 0.0, True, 5, 1e-7, 1.0, None, None)
+    with pytest.raises(ValueError, match="rows, cols"):
+        binding.moe_norm_backward(rms, x, torch.zeros(8), None, None, None, None, None, None, None, None)
