@@ -43,28 +43,34 @@ struct Vec<float> {
   typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(4)));
 };
 
-// the vector of a row that starts at element c (c < cols); elements past the
-// row's end are 0
+// the vector of a row that starts at element c (c < cols), as it is stored;
+// elements past the row's end are 0
+template <typename T>
+__device__ __forceinline__ u32x4 load_raw(const T* row, int c, int cols) {
+  constexpr int N = Vec<T>::kN;
+  if (c + N <= cols) return *reinterpret_cast<const typename Vec<T>::raw*>(row + c);
+  u32x4 w = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (c + i < cols) {
+      if constexpr (N == 8) w[i >> 1] |= static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
+      else w[i] = __float_as_uint(row[c + i]);
+    }
+  return w;
+}
+
+template <int N>
+__device__ __forceinline__ void unpack(const u32x4& w, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (N == 8) v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    else v[i] = __uint_as_float(w[i]);
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void load_vec(const T* row, int c, int cols, float (&v)[Vec<T>::kN]) {
-  constexpr int N = Vec<T>::kN;
-  if (c + N <= cols) {
-    const u32x4 w = *reinterpret_cast<const typename Vec<T>::raw*>(row + c);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (N == 8) v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-      else v[i] = __uint_as_float(w[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = 0.0f;
-      if (c + i < cols) {
-        if constexpr (N == 8) v[i] = bf16_to_f32(row[c + i]);
-        else v[i] = row[c + i];
-      }
-    }
-  }
+  unpack(load_raw(row, c, cols), v);
 }
 
 template <typename T>
@@ -104,7 +110,9 @@ __device__ __forceinline__ void group_sum(float (&s)[K], float* red) {
 #pragma unroll
     for (int k = 0; k < K; ++k) s[k] += __shfl_xor(s[k], d);
   if constexpr (WPR > 1) {
-    const int w = threadIdx.x >> 6;                   // a group is the whole workgroup
+    // (the barriers are the workgroup's: its groups take them together)
+    const int w = (threadIdx.x >> 6) % WPR;
+    red += (threadIdx.x >> 6) / WPR * K * WPR;
     __syncthreads();                                  // the last call's reads are done
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -121,8 +129,9 @@ __device__ __forceinline__ void group_sum(float (&s)[K], float* red) {
   }
 }
 
-constexpr int threads_of(int wpr) { return wpr > 4 ? 64 * wpr : 256; }
-constexpr int groups_of(int wpr) { return threads_of(wpr) / (64 * wpr); }     // rows at a time per workgroup
+// rows at a time per workgroup
+constexpr int groups_of(int wpr, bool backward) { return wpr == 1 ? 4 : wpr == 4 && backward ? 2 : 1; }
+constexpr int threads_of(int wpr, bool backward) { return 64 * wpr * groups_of(wpr, backward); }
 
 struct NormArgs {
   const void* x;
@@ -142,8 +151,9 @@ struct NormArgs {
 };
 
 template <typename T, int CH, int WPR>
-__global__ __launch_bounds__(threads_of(WPR)) void norm_forward_kernel(NormArgs a) {
-  constexpr int N = Vec<T>::kN, kT = 64 * WPR, kG = groups_of(WPR);
+__global__ __launch_bounds__(threads_of(WPR, false)) void norm_forward_kernel(NormArgs a) {
+  constexpr int N = Vec<T>::kN, kT = 64 * WPR, kG = groups_of(WPR, false);
+  static_assert(WPR == 1 || kG == 1, "the groups of a workgroup would part at a barrier");
   __shared__ float red[WPR];
   const int t = threadIdx.x % kT, grp = threadIdx.x / kT;
   const int cols = a.cols;
@@ -219,9 +229,9 @@ __global__ __launch_bounds__(threads_of(WPR)) void norm_forward_kernel(NormArgs 
 }
 
 template <typename T, int CH, int WPR, bool BETA>
-__global__ __launch_bounds__(threads_of(WPR)) void norm_backward_kernel(NormArgs a) {
-  constexpr int N = Vec<T>::kN, kT = 64 * WPR, kG = groups_of(WPR);
-  __shared__ float red[2 * WPR];
+__global__ __launch_bounds__(threads_of(WPR, true)) void norm_backward_kernel(NormArgs a) {
+  constexpr int N = Vec<T>::kN, kT = 64 * WPR, kG = groups_of(WPR, true);
+  __shared__ float red[2 * WPR * kG];
   __shared__ float fold[kG > 1 ? (kG - 1) * kT * N : 1];
   const int t = threadIdx.x % kT, grp = threadIdx.x / kT;
   const int cols = a.cols;
@@ -236,53 +246,71 @@ __global__ __launch_bounds__(threads_of(WPR)) void norm_backward_kernel(NormArgs
       if constexpr (BETA) db[k][i] = 0.0f;
     }
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kG + grp; row < a.rows;
-       row += static_cast<int64_t>(gridDim.x) * kG) {
+  // a row's input, loaded while the row before it is worked on
+  struct Row {
+    u32x4 x[CH], dy[CH], ds[CH];
+    float mean, rstd;
+  } cur, next;
+  auto load = [&](int64_t row0, Row& q) __attribute__((always_inline)) {
+    // (a group past the last row goes through the barriers with zeros)
+    const bool live = row0 + grp < a.rows;
+    const int64_t row = live ? row0 + grp : a.rows - 1;
     const size_t at = static_cast<size_t>(row) * cols;
-    float h[CH][N], g[CH][N];
-    const float mean = a.layer ? a.mean[row] : 0.0f, rstd = a.rstd[row];
-    float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = (k * kT + t) * N;
-      if (c < cols) {
-        load_vec<T>(static_cast<const T*>(a.x) + at, c, cols, h[k]);
-        load_vec<T>(static_cast<const T*>(a.dy) + at, c, cols, g[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) h[k][i] = g[k][i] = 0.0f;
+      q.x[k] = q.dy[k] = q.ds[k] = u32x4{0, 0, 0, 0};
+      if (live && c < cols) {
+        q.x[k] = load_raw(static_cast<const T*>(a.x) + at, c, cols);
+        q.dy[k] = load_raw(static_cast<const T*>(a.dy) + at, c, cols);
+        if (a.residual != nullptr) q.ds[k] = load_raw(static_cast<const T*>(a.residual) + at, c, cols);
       }
     }
+    q.mean = a.layer ? a.mean[row] : 0.0f;
+    q.rstd = a.rstd[row];
+  };
+  // (the widest rows leave no registers for it)
+  constexpr bool kEarly = WPR < 16 || CH == 1;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kG;
+  if (kEarly) load(static_cast<int64_t>(blockIdx.x) * kG, cur);
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kG; row0 < a.rows; row0 += stride) {
+    // (dx may be dy, x or dsum itself: other rows than those still to be read)
+    if (!kEarly) load(row0, cur);
+    else if (row0 + stride < a.rows) load(row0 + stride, next);
+    float h[CH][N], g[CH][N];
+    float s[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < CH; ++k)
+    for (int k = 0; k < CH; ++k) {
+      unpack(cur.x[k], h[k]);
+      unpack(cur.dy[k], g[k]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         // (past the row's end g is 0, so h adds nothing there)
-        h[k][i] = (h[k][i] - mean) * rstd;
+        h[k][i] = (h[k][i] - cur.mean) * cur.rstd;
         dg[k][i] = fmaf(g[k][i], h[k][i], dg[k][i]);
         if constexpr (BETA) db[k][i] += g[k][i];
         g[k][i] *= gm[k][i];
         s[0] = fmaf(g[k][i], h[k][i], s[0]);
         s[1] += g[k][i];
       }
+    }
     group_sum<WPR, 2>(s, red);
     const float mh = s[0] * inv, m1 = a.layer ? s[1] * inv : 0.0f;
+    if (row0 + grp < a.rows) {
+      T* dx = static_cast<T*>(a.y) + static_cast<size_t>(row0 + grp) * cols;
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = (k * kT + t) * N;
-      if (c < cols) {
-        float r[N];
-        if (a.residual != nullptr) {
-          load_vec<T>(static_cast<const T*>(a.residual) + at, c, cols, r);
-        } else {
+      for (int k = 0; k < CH; ++k) {
+        const int c = (k * kT + t) * N;
+        if (c < cols) {
+          float r[N];
+          unpack(cur.ds[k], r);
 #pragma unroll
-          for (int i = 0; i < N; ++i) r[i] = 0.0f;
+          for (int i = 0; i < N; ++i) r[i] = fmaf(cur.rstd, g[k][i] - m1 - h[k][i] * mh, r[i]);
+          store_vec<T>(dx, c, cols, r);
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = fmaf(rstd, g[k][i] - m1 - h[k][i] * mh, r[i]);
-        store_vec<T>(static_cast<T*>(a.y) + at, c, cols, r);
       }
     }
+    if (kEarly) cur = next;
   }
   if (a.part == nullptr) return;
   // the workgroup's column sums: its groups' added in order, then stored
@@ -320,73 +348,87 @@ __global__ __launch_bounds__(threads_of(WPR)) void norm_backward_kernel(NormArgs
     }
 }
 
-// out[c] = sum over workgroups of part[w][b][c], in order: 16 slices of the
-// workgroups, then the slices
-constexpr int kFoldCols = 64, kFoldSlices = 16;
+// out[c] = sum over workgroups of part[w][b][c]: 64 slices of the workgroups
+// for each of 16 columns, then the slices, both in a fixed order.  Bound by
+// latency: every thread's loads are in flight together.
+constexpr int kFoldCols = 16, kFoldSlices = 64;
 
 __global__ __launch_bounds__(kFoldCols* kFoldSlices) void norm_fold_kernel(const float* part, int groups, int nb,
                                                                            int cols, float* dgamma, float* dbeta) {
-  __shared__ float red[kFoldSlices][kFoldCols];
+  __shared__ float red[kFoldSlices * kFoldCols];
   const int c = blockIdx.x * kFoldCols + threadIdx.x % kFoldCols, sl = threadIdx.x / kFoldCols;
   const int b = blockIdx.y;
   float* out = b ? dbeta : dgamma;
   float s = 0.0f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 8
     for (int w = sl; w < groups; w += kFoldSlices) s += part[(static_cast<size_t>(w) * nb + b) * cols + c];
-  red[sl][threadIdx.x % kFoldCols] = s;
-  __syncthreads();
-  if (sl == 0 && c < cols && out != nullptr) {
-    for (int i = 1; i < kFoldSlices; ++i) s += red[i][threadIdx.x];
-    out[c] = s;
   }
+  red[threadIdx.x] = s;
+#pragma unroll
+  for (int n = kFoldSlices / 4; n >= 1; n /= 4) {
+    __syncthreads();
+    if (sl < n) {
+      s = ((red[threadIdx.x] + red[threadIdx.x + n * kFoldCols]) +
+           (red[threadIdx.x + 2 * n * kFoldCols] + red[threadIdx.x + 3 * n * kFoldCols]));
+    }
+    __syncthreads();
+    if (sl < n) red[threadIdx.x] = s;
+  }
+  if (sl == 0 && c < cols && out != nullptr) out[c] = s;
 }
 
-// Vectors per thread and waves per row.  One wave per row needs no barrier;
-// more waves per row spread the few rows of a decode batch.
+// Vectors per thread and waves per row.  Batches of many rows take the fewest
+// waves whose registers leave enough of them resident (32768 x 2048 in bf16,
+// forward: 99 us with one vector a thread and 4 waves a row, 124 us with four
+// vectors and one wave); few rows are spread over more waves, for latency.
 struct NormForm {
   int ch, wpr;
 };
 
-NormForm form_of(int64_t rows, int cols, int n, bool backward) {
+NormForm form_of(int64_t rows, int cols, int n) {
   const int vecs = (cols + n - 1) / n;
   auto fits = [&](int ch, int wpr) { return vecs <= ch * wpr * 64; };
-  const int most = backward ? 2 : 4;
-  if (rows >= 1024) {
-    for (int ch = 1; ch <= most; ch *= 2)
-      if (fits(ch, 1)) return {ch, 1};
-  } else if (fits(1, 1)) {
-    return {1, 1};
-  }
-  for (int ch = 1; ch <= (rows >= 1024 ? most : 1); ch *= 2)
+  if (fits(1, 1)) return {1, 1};
+  const int most = rows >= 1024 ? 2 : 1;
+  if (rows >= 1024 && fits(2, 1)) return {2, 1};
+  for (int ch = 1; ch <= most; ch *= 2)
     if (fits(ch, 4)) return {ch, 4};
   for (int ch = 1; ch <= 4; ch *= 2)
     if (fits(ch, 16)) return {ch, 16};
   return {0, 0};
 }
 
+// Workgroups: what the CUs hold at once by the kernels' registers, and the
+// same number of rows for each (2048 workgroups instead of 1536 for the batch
+// above, a second round for some: 124 us instead of 99).
 int grid_of(int64_t rows, NormForm f, bool backward) {
-  const int64_t need = (rows + groups_of(f.wpr) - 1) / groups_of(f.wpr);
-  const int64_t most = backward ? (f.wpr == 16 ? 256 : 512) : (f.wpr == 16 ? 512 : 2048);
-  return static_cast<int>(need < most ? need : most);
+  const int64_t need = (rows + groups_of(f.wpr, backward) - 1) / groups_of(f.wpr, backward);
+  const int per_cu = backward ? (f.wpr == 16 ? 1 : f.wpr == 4 ? (f.ch == 1 ? 2 : 1) : f.ch == 1 ? 4 : 3)
+                              : (f.wpr == 16 ? 1 : f.ch == 1 ? 6 : 4);
+  const int64_t most = 256 * per_cu;
+  if (need <= most) return static_cast<int>(need);
+  const int64_t each = (need + most - 1) / most;
+  return static_cast<int>((need + each - 1) / each);
 }
 
 template <typename T, int CH, int WPR>
 void launch_fwd(const NormArgs& a, int grid, hipStream_t st) {
-  norm_forward_kernel<T, CH, WPR><<<grid, threads_of(WPR), 0, st>>>(a);
+  norm_forward_kernel<T, CH, WPR><<<grid, threads_of(WPR, false), 0, st>>>(a);
 }
 
 template <typename T, int CH, int WPR>
 void launch_bwd(const NormArgs& a, int grid, bool beta, hipStream_t st) {
-  if (beta) norm_backward_kernel<T, CH, WPR, true><<<grid, threads_of(WPR), 0, st>>>(a);
-  else norm_backward_kernel<T, CH, WPR, false><<<grid, threads_of(WPR), 0, st>>>(a);
+  if (beta) norm_backward_kernel<T, CH, WPR, true><<<grid, threads_of(WPR, true), 0, st>>>(a);
+  else norm_backward_kernel<T, CH, WPR, false><<<grid, threads_of(WPR, true), 0, st>>>(a);
 }
 
 template <typename T, typename F>
 void with_form(NormForm f, F&& go) {
 #define MOE_NORM_CASE(CH, WPR) \
   if (f.ch == CH && f.wpr == WPR) return go(std::integral_constant<int, CH>{}, std::integral_constant<int, WPR>{});
-  MOE_NORM_CASE(1, 1) MOE_NORM_CASE(2, 1) MOE_NORM_CASE(4, 1)
-  MOE_NORM_CASE(1, 4) MOE_NORM_CASE(2, 4) MOE_NORM_CASE(4, 4)
+  MOE_NORM_CASE(1, 1) MOE_NORM_CASE(2, 1)
+  MOE_NORM_CASE(1, 4) MOE_NORM_CASE(2, 4)
   MOE_NORM_CASE(1, 16) MOE_NORM_CASE(2, 16)
   if constexpr (sizeof(T) == 4) { MOE_NORM_CASE(4, 16) }
 #undef MOE_NORM_CASE
@@ -398,7 +440,7 @@ size_t norm_workspace_bytes(int64_t rows, int cols) {
   // the most workgroups of any form, two sums each
   size_t most = 0;
   for (int n = 4; n <= 8; n += 4) {
-    const NormForm f = form_of(rows, cols, n, true);
+    const NormForm f = form_of(rows, cols, n);
     const size_t b = static_cast<size_t>(grid_of(rows, f, true)) * 2 * cols * sizeof(float);
     most = b > most ? b : most;
   }
@@ -421,7 +463,7 @@ hipError_t launch_norm_forward(bool layer, int64_t rows, int cols, bool bf16, co
   a.cols = cols;
   a.layer = layer;
   a.eps = eps;
-  const NormForm f = form_of(rows, cols, bf16 ? 8 : 4, false);
+  const NormForm f = form_of(rows, cols, bf16 ? 8 : 4);
   const int grid = grid_of(rows, f, false);
   if (bf16) with_form<bf16_t>(f, [&](auto ch, auto w) { launch_fwd<bf16_t, ch(), w()>(a, grid, st); });
   else with_form<float>(f, [&](auto ch, auto w) { launch_fwd<float, ch(), w()>(a, grid, st); });
@@ -446,7 +488,7 @@ hipError_t launch_norm_backward(bool layer, int64_t rows, int cols, bool bf16, c
   a.part = any ? static_cast<float*>(workspace) : nullptr;
   int grid = 0;
   if (rows > 0) {
-    const NormForm f = form_of(rows, cols, bf16 ? 8 : 4, true);
+    const NormForm f = form_of(rows, cols, bf16 ? 8 : 4);
     grid = grid_of(rows, f, true);
     if (bf16) with_form<bf16_t>(f, [&](auto ch, auto w) { launch_bwd<bf16_t, ch(), w()>(a, grid, beta, st); });
     else with_form<float>(f, [&](auto ch, auto w) { launch_bwd<float, ch(), w()>(a, grid, beta, st); });

@@ -33,7 +33,9 @@
 //     otherwise be the largest error;
 //   * x is stored as fp16 hi + lo (22 bits).  M x and diag(d) x read hi (the
 //     latter as MFMAs with a diagonal operand, in the stage that holds the
-//     rows), the epilogue adds d_i lo_ij.
+//     rows), the epilogue adds d_i lo_ij.  The x before the last step has no
+//     low part: what its rounding adds is amplified by a at most (first line of
+//     the table above 1.8e-3 -> 1.9e-3; without it in the last two 2.8e-3).
 // Powers of two keep fp16 away from its subnormals: x and R are stored times
 // 2^12 (|x|, |R| < 2), Q and Q2 Q1 times 2^8 (|Q2 Q1| <= a^2 = 12).
 //
@@ -70,16 +72,17 @@ constexpr int kStages = 4;            // stages of the ring
 constexpr int kOXcds = 8;
 constexpr int kMinPad = 128;          // smallest padded side: a tile has at least kStages stages
 
-enum { kGram = 0, kPoly = 1, kMul = 2, kApply = 3, kFinal = 4 };
+// kFinal: x <- P x into the caller's matrix, x without a low part (kFinalLo: with)
+enum { kGram = 0, kPoly = 1, kMul = 2, kApply = 3, kFinal = 4, kFinalLo = 5 };
 
 struct OrthJob {
   const _Float16* p;        // row operand, [rows / 32][K / 16] blocks
-  const _Float16* q;        // column operand; kApply / kFinal: x hi, [K / 32][n / 16] blocks
-  const _Float16* lo;       // kApply / kFinal: x lo
+  const _Float16* q;        // column operand; kApply, kFinal, kFinalLo: x hi, [K / 32][n / 16] blocks
+  const _Float16* lo;       // kApply / kFinalLo: x lo
   const float* dp;          // diagonals of p and q
   const float* dq;
   _Float16* out;            // kFinal: unused
-  _Float16* out_lo;         // kApply: the low part
+  _Float16* out_lo;         // kApply: the low part, or null
   float* dout;
   float sp, sq, so;         // stored scales of p, q and out
 };
@@ -151,7 +154,7 @@ __device__ __forceinline__ void triangle(int l, int& i, int& j) {
 
 // 8 consecutive elements of an output row from their sums of products v, in the
 // output's stored scale.  a: the column operand's elements at this place (x's
-// low part in kApply and kFinal), b: the row operand's; dpi, dq: the operands'
+// low part in kApply and kFinalLo), b: the row operand's; dpi, dq: the operands'
 // diagonals at this row and these columns.
 template <int MODE>
 __device__ __forceinline__ void finish(float (&v)[8], const f16x8& a, const f16x8& b, float dpi, const float* dq,
@@ -171,6 +174,9 @@ __device__ __forceinline__ void finish(float (&v)[8], const f16x8& a, const f16x
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       v[e] = fmaf(static_cast<float>(b[e]), dq[e] * fp, fmaf(static_cast<float>(a[e]), u, v[e] * f));
+  } else if constexpr (MODE == kFinal) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= 1.0f / kSQ;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = fmaf(static_cast<float>(a[e]), dpi, v[e] * (1.0f / kSQ));
@@ -258,6 +264,7 @@ template <int WB, int MODE>
 __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(OrthArgs g) {
   constexpr bool kSym = MODE <= kMul;
   constexpr bool kTr = !kSym;
+  constexpr bool kOut = MODE >= kFinal;
   constexpr int TB = 2 * WB;
   constexpr int kOpBytes = TB * 2048;               // one operand of a stage
   constexpr int kStage = 2 * kOpBytes;
@@ -452,7 +459,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     // byte offset of block (rb, cb)'s 2 KB (two 16-column blocks)
     auto at_block = [&](int rb, int cb) { return (static_cast<size_t>(rb) * o16 + 2 * cb) * 1024; };
     // blocks q go down the tile's columns (kFinal: along the caller's rows)
-    const bool across = MODE == kFinal && !g.tall;
+    const bool across = kOut && !g.tall;
     struct Ahead {
       f16x8 a[2], b[MODE == kMul ? 2 : 1];
     } pre[kAhead];
@@ -463,7 +470,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       v[1] = *reinterpret_cast<const f16x8*>(p + 1024 + run1);
     };
     auto fetch = [&](int q) __attribute__((always_inline)) {
-      if constexpr (MODE != kGram) {
+      if constexpr (MODE != kGram && MODE != kFinal) {
         // (blocks past the matrix: its last one, in bounds and not used)
         const int rb = min(row_block(across ? q / WB : q % WB), g.mb - 1);
         const int cb = min(col_block(across ? q % WB : q / WB), g.nb - 1);
@@ -527,7 +534,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     u32x4 ob[2][2];                                 // kFinal: the two blocks of a 64-element piece of rows
 #pragma unroll
     for (int q = 0; q < kBlocks; ++q) {
-      const int i = MODE == kFinal ? q / WB : q % WB, j = MODE == kFinal ? q % WB : q / WB;
+      const int i = kOut ? q / WB : q % WB, j = kOut ? q % WB : q / WB;
       // (kFinal of a tall matrix: the same q goes down the columns)
       auto block = [&](int bi, int bj, f32x16& c) __attribute__((always_inline)) {
         // read this block's accumulators only now: without the (empty) asm the
@@ -564,14 +571,14 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
             }
           }
         }
-        if constexpr (MODE != kFinal) {
+        if constexpr (!kOut) {
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             w[p] = to_f16(v[p]);
             if constexpr (MODE == kApply) wl[p] = low_part(v[p], w[p]);
           }
         }
-        if constexpr (MODE != kFinal) {
+        if constexpr (!kOut) {
           if (inside) {
             auto put = [&](_Float16* m, int row, int col, const f16x8 (&x)[2]) __attribute__((always_inline)) {
               unsigned char* p = uniform(reinterpret_cast<unsigned char*>(m + cur.mat * g.out_stride) + at_block(row, col));
@@ -579,7 +586,9 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
               *reinterpret_cast<f16x8*>(p + 1024 + run1) = x[1];
             };
             put(jb.out, rb, cb, w);
-            if constexpr (MODE == kApply) put(jb.out_lo, rb, cb, wl);
+            if constexpr (MODE == kApply) {
+              if (jb.out_lo != nullptr) put(jb.out_lo, rb, cb, wl);
+            }
             if constexpr (kSym) {
               if (cur.rb != cur.cb) {               // the mirror image of a tile below the diagonal
                 *reinterpret_cast<f16x8*>(stg + run0) = w[0];
@@ -594,7 +603,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
           for (int p = 0; p < 2; ++p) ob[q & 1][p] = to_bf16(v[p], g.scale / kSX);
         }
       };
-      if constexpr (MODE != kFinal) {
+      if constexpr (!kOut) {
         if (i == 0 && j + 1 < WB) fetch_dq(j + 1);
         block(i, j, acc[i][j]);
       } else if (!g.tall) {
@@ -602,7 +611,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       } else {
         block(j, i, acc[j][i]);
       }
-      if constexpr (MODE == kFinal) {
+      if constexpr (kOut) {
         // two blocks make 64 consecutive elements of 32 of the caller's rows:
         // through LDS (chunks XOR-swizzled by row / 2), then whole 128-byte
         // segments, 8 rows a store
@@ -660,6 +669,7 @@ template <int MODE>
 __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   constexpr bool kSym = MODE <= kMul;
   constexpr bool kTr = !kSym;
+  constexpr bool kOut = MODE >= kFinal;
   constexpr int kHalf = kSWaves / 2;
   // the waves' sums (half of them at a time); before that, x's blocks; behind
   // it, finished blocks on their way to a transposed store
@@ -779,7 +789,7 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   f16x8 ea{}, eb{};
   float dpi = 0.0f, dq[8] = {}, dqi = 0.0f;
   if constexpr (MODE != kGram) {
-    ea = *reinterpret_cast<const f16x8*>((kSym ? jb.q : jb.lo) + mat * g.q_stride + blk);
+    if constexpr (MODE != kFinal) ea = *reinterpret_cast<const f16x8*>((kSym ? jb.q : jb.lo) + mat * g.q_stride + blk);
     if constexpr (MODE == kMul) eb = *reinterpret_cast<const f16x8*>(jb.p + mat * g.p_stride + blk);
     dpi = dpm[32 * min(rb, g.mb - 1) + r];
   }
@@ -825,11 +835,13 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
     }
   }
   unsigned char* flip = smem + kHalf * 16384 + unit * 2048;
-  if constexpr (MODE != kFinal) {
+  if constexpr (!kOut) {
     const f16x8 w = to_f16(v);
     if (inside) {
       *reinterpret_cast<f16x8*>(jb.out + mat * g.out_stride + blk) = w;
-      if constexpr (MODE == kApply) *reinterpret_cast<f16x8*>(jb.out_lo + mat * g.out_stride + blk) = low_part(v, w);
+      if constexpr (MODE == kApply) {
+        if (jb.out_lo != nullptr) *reinterpret_cast<f16x8*>(jb.out_lo + mat * g.out_stride + blk) = low_part(v, w);
+      }
     }
     if constexpr (kSym) {
       if (rb0 != cb0) {                               // the mirror image
@@ -1580,15 +1592,18 @@ hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, co
     a.job = j;
     launch_mode<kMul>(a, st);
   };
-  auto apply = [&](int q, bool last) {          // x <- S[q] x
+  bool has_lo = true;                           // x_0 has a low part
+  auto apply = [&](int q, int after) {          // x <- S[q] x, with `after` steps to follow
     OrthArgs a = base;
     a.nb = p.np / 32;
     a.K = p.mp;
     a.p_stride = ss;
     a.q_stride = a.out_stride = xs;
-    a.job = {S[q], X[xi], X[xi + 1], D[q], nullptr, X[xi ^ 2], X[(xi ^ 2) + 1], nullptr, kSQ, kSX, kSX};
-    if (last) launch_mode<kFinal>(a, st);
-    else launch_mode<kApply>(a, st);
+    a.job = {S[q], X[xi], X[xi + 1], D[q], nullptr, X[xi ^ 2], after > 1 ? X[(xi ^ 2) + 1] : nullptr, nullptr, kSQ, kSX, kSX};
+    if (after > 0) launch_mode<kApply>(a, st);
+    else if (has_lo) launch_mode<kFinalLo>(a, st);
+    else launch_mode<kFinal>(a, st);
+    has_lo = after > 1;
     xi ^= 2;
   };
 
@@ -1601,12 +1616,12 @@ hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, co
     poly(V);                                    // Q2
     mul(product(V, kSQ, U, kSQ, T, kSQ));       // Q2 Q1
     left -= 2;
-    apply(T, left == 0);
+    apply(T, left);
   }
   while (left > 0) {
     gram();
     poly(U);
-    apply(U, --left == 0);
+    apply(U, --left);
   }
   return hipGetLastError();
 }
