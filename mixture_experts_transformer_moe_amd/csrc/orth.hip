@@ -141,6 +141,10 @@ __device__ __forceinline__ f16x8 tr_run(const unsigned char* b, int kk, int lane
   return __builtin_bit_cast(f16x8, v);
 }
 
+// what a wave computes of a stage: all its blocks, those on and below the
+// diagonal, none
+constexpr int kAllTag = -1, kLowerTag = -2, kIdleTag = -3;
+
 constexpr int wait_vm(int n) { return vmcnt_only(n > 63 ? 63 : n); }
 constexpr int kWaitLds = 15 | (7 << 4) | (0 << 8) | (3 << 14);     // lgkmcnt(0) only
 
@@ -250,7 +254,7 @@ __device__ __forceinline__ void gather_columns(const float (&c)[8], float (&v)[8
 }
 
 // One product of the iteration.  A tile is TB x TB blocks of 32 (TB = 2 WB),
-// each wave owns WB x WB of them.  The symmetric modes compute the tiles on
+// each wave owns WB x WB of them.  The symmetric modes compute the blocks on
 // and below the diagonal and store the mirror image of those below.
 //
 // Schedule: a persistent grid walks the tiles in rounds, each round cut into 8
@@ -398,12 +402,14 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
                             : g.job.dp[static_cast<size_t>(cur.mat) * g.d_stride +
                                        32 * min(cur.rb + wr * WB + i, g.mb - 1) + (lane & 31)];
 
-    auto step = [&](const Frag& f, auto&& op) __attribute__((always_inline)) {
+    auto step = [&](const Frag& f, auto tag, auto&& op) __attribute__((always_inline)) {
+      constexpr bool lower = decltype(tag)::value == kLowerTag;
 #pragma unroll
       for (int i = 0; i < WB; ++i)
 #pragma unroll
         for (int j = 0; j < WB; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[WB + j], f[i], acc[i][j], 0, 0, 0);
+          if (!lower || j <= i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[WB + j], f[i], acc[i][j], 0, 0, 0);
           op(WB * i + j);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -425,11 +431,11 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       for (int j = 0; j < WB; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[WB + j], e, acc[i][j], 0, 0, 0);
     };
-    auto stage = [&](auto own_tag) __attribute__((always_inline)) {
-      constexpr int own = decltype(own_tag)::value;   // row block whose rows the stage holds, or -1
+    auto stage = [&](auto tag) __attribute__((always_inline)) {
+      constexpr int own = decltype(tag)::value;       // row block whose rows the stage holds, or a tag
       const int b0 = ring;
       const int b1 = (ring + 1) & (kStages - 1);
-      step(f0, [&](int k) __attribute__((always_inline)) {
+      if constexpr (own != kIdleTag) step(f0, tag, [&](int k) __attribute__((always_inline)) {
         if (k % kEvery == 0) read_op(b0, 1, k / kEvery, f1);
       });
       if constexpr (own >= 0) diagonal(own, 0, f0);
@@ -440,10 +446,15 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       __builtin_amdgcn_s_waitcnt(kWaitLds);
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      step(f1, [&](int k) __attribute__((always_inline)) {
-        if (k % kEvery == 0) read_op(b1, 0, k / kEvery, f0);
-        if (k % kEvery == kEvery - 1) issue(b0, k / kEvery);
-      });
+      if constexpr (own != kIdleTag) {
+        step(f1, tag, [&](int k) __attribute__((always_inline)) {
+          if (k % kEvery == 0) read_op(b1, 0, k / kEvery, f0);
+          if (k % kEvery == kEvery - 1) issue(b0, k / kEvery);
+        });
+      } else {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) issue(b0, k);
+      }
       if constexpr (own >= 0) diagonal(own, 1, f1);
       advance();
       ring = b1;
@@ -504,12 +515,29 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       for (int q = 0; q < kAhead; ++q) fetch(q);
       point(tn >= 0 ? nxt : cur);
     };
-    using None = std::integral_constant<int, -1>;
+    using None = std::integral_constant<int, kAllTag>;
     if constexpr (kSym) {
-      for (int x = kStages; x < nkb; ++x) stage(None{});
-      turn();
+      auto loop = [&](auto tag) __attribute__((always_inline)) {
+        for (int x = kStages; x < nkb; ++x) stage(tag);
+        turn();
 #pragma unroll 1
-      for (int x = 0; x < kStages; ++x) stage(None{});
+        for (int x = 0; x < kStages; ++x) stage(tag);
+      };
+      // In a tile of R on the diagonal the blocks above it are left out (the
+      // chip runs at its power limit here, so MFMAs saved are time saved: 32
+      // matrices of 2048 x 4096 542 -> 518 us): the upper right wave only
+      // loads, the two waves on the diagonal compute their lower blocks.  The
+      // other modes' epilogue loads would cross the branches, which waits for
+      // them (the same matrices, Q: 314 -> 377 us).
+      if (MODE != kGram || cur.rb != cur.cb || wr > wc) {
+        loop(None{});
+      } else if (wr == wc) {
+        loop(std::integral_constant<int, kLowerTag>{});
+      } else {
+        loop(std::integral_constant<int, kIdleTag>{});
+#pragma unroll
+        for (int k = 0; k < 2 * WB; ++k) read_op(ring, 0, k, f0);
+      }
     } else {
       // the stages of the wave's own row blocks apart (no branch may hold
       // MFMAs: the accumulators would leave their registers)
@@ -541,6 +569,8 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
         // compiler copies all of them out of the AGPRs at once, and spills
         if constexpr (WB == 4) asm volatile("" : "+a"(c));
         const int rb = row_block(bi), cb = col_block(bj);
+        // (the other modes' fetches below must not sit in a branch)
+        if (MODE == kGram && rb < cb) return;
         const bool inside = rb < g.mb && cb < g.nb;
         const bool diag = kSym && rb == cb;
         // 8 consecutive columns a lane: 16 p + 8 h + 0..7
@@ -585,12 +615,12 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
               *reinterpret_cast<f16x8*>(p + run0) = x[0];
               *reinterpret_cast<f16x8*>(p + 1024 + run1) = x[1];
             };
-            put(jb.out, rb, cb, w);
+            if (!kSym || rb >= cb) put(jb.out, rb, cb, w);
             if constexpr (MODE == kApply) {
               if (jb.out_lo != nullptr) put(jb.out_lo, rb, cb, wl);
             }
             if constexpr (kSym) {
-              if (cur.rb != cur.cb) {               // the mirror image of a tile below the diagonal
+              if (rb > cb) {                        // the mirror image of a block below the diagonal
                 *reinterpret_cast<f16x8*>(stg + run0) = w[0];
                 *reinterpret_cast<f16x8*>(stg + 1024 + run1) = w[1];
                 const f16x8 t[2] = {tr_run(stg, 0, lane), tr_run(stg, 1, lane)};
