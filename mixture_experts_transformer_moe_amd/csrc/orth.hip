@@ -685,29 +685,31 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
 }
 
 // The same products for few tiles, where a tile's latency counts and not the
-// matrix cores' rate: tiles of 64 x 64, a workgroup of 8 waves each, which
-// share out the stages of K.  Operands go from global memory straight into
+// matrix cores' rate: tiles of SB x SB blocks of 32, a workgroup of 8 waves
+// each, which share out the stages of K.  Operands go from global memory straight into
 // registers in operand order (x's blocks through 4 KB of LDS, for the
-// transposing read), the loads of 2 to 4 stages a wave in flight, no barrier
+// transposing read), the loads of 2 to 8 stages a wave in flight, no barrier
 // until the waves' sums are joined through LDS in a fixed order.  Wave u then
 // finishes 32 rows x 16 columns, half of block u / 2.
 constexpr int kSThreads = 512;
 constexpr int kSWaves = kSThreads / 64;
-constexpr int kSAhead = 2;             // stages a wave loads at once, two sets in turn
 
-template <int MODE>
+template <int SB, int MODE>
 __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   constexpr bool kSym = MODE <= kMul;
   constexpr bool kTr = !kSym;
   constexpr bool kOut = MODE >= kFinal;
   constexpr int kHalf = kSWaves / 2;
+  constexpr int kAcc = SB * SB;                       // blocks of a tile
+  constexpr int kAhead = SB == 1 ? 4 : 2;             // stages a wave loads at once, two sets in turn
   // the waves' sums (half of them at a time); before that, x's blocks; behind
   // it, finished blocks on their way to a transposed store
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[kHalf * 16384 + 8192];
+  __shared__ __attribute__((aligned(1024))) unsigned char
+      smem[(kAcc * kHalf * 4096 > kSWaves * SB * 2048 ? kAcc * kHalf * 4096 : kSWaves * SB * 2048) + kAcc * 2048];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  const int mt = (g.mb + 1) / 2, nt = (g.nb + 1) / 2;
+  const int mt = (g.mb + SB - 1) / SB, nt = (g.nb + SB - 1) / SB;
   const int per_mat = kSym ? mt * (mt + 1) / 2 : mt * nt;
   const int total = per_mat * g.count;
   // runs of consecutive tiles on the XCDs (workgroup b runs on XCD b mod 8)
@@ -723,8 +725,8 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
     i0 = l - j0 * mt;
   }
   // (x's row tiles are all whole, as in the kernel above)
-  const int rb0 = __builtin_amdgcn_readfirstlane(kTr ? min(2 * i0, g.mb - 2) : 2 * i0);
-  const int cb0 = __builtin_amdgcn_readfirstlane(2 * j0);
+  const int rb0 = __builtin_amdgcn_readfirstlane(kTr ? min(SB * i0, g.mb - SB) : SB * i0);
+  const int cb0 = __builtin_amdgcn_readfirstlane(SB * j0);
   const OrthJob& jb = g.job;
   const unsigned char* P = reinterpret_cast<const unsigned char*>(jb.p + mat * g.p_stride);
   const unsigned char* Q = reinterpret_cast<const unsigned char*>(jb.q + mat * g.q_stride);
@@ -733,22 +735,22 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   const int run[2] = {run_off(r, h, 0), run_off(r, h, 1)};
   const float* dpm = MODE == kGram ? nullptr : jb.dp + static_cast<size_t>(mat) * g.d_stride;
 
-  f32x16 acc[2][2];
+  f32x16 acc[SB][SB];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < SB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{0.f};
-  unsigned char* mine = smem + wave * 4096;
+    for (int j = 0; j < SB; ++j) acc[i][j] = f32x16{0.f};
+  unsigned char* mine = smem + wave * SB * 2048;
   struct Set {
-    f16x8 p[kSAhead][2][2], q[kSAhead][2][2];
+    f16x8 p[kAhead][SB][2], q[kAhead][SB][2];
   };
   auto load = [&](int base, Set& t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < kSAhead; ++s) {
+    for (int s = 0; s < kAhead; ++s) {
       // (a stage past the end loads the last one again: in bounds, not used)
       const int kb = min(base + s * kSWaves, nkb - 1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < SB; ++i) {
         const unsigned char* ps = P + min(rb0 + i, g.mb - 1) * row_bytes + kb * 2048;
         const int cb = min(cb0 + i, g.nb - 1);
         const unsigned char* qs = kTr ? Q + (static_cast<size_t>(kb) * g.nb + cb) * 2048 : Q + cb * row_bytes + kb * 2048;
@@ -762,24 +764,24 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   };
   auto use = [&](int base, Set& t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < kSAhead; ++s) {
+    for (int s = 0; s < kAhead; ++s) {
       const int kb = base + s * kSWaves;
       if (kb < nkb) {
         if constexpr (kTr) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < SB; ++j)
 #pragma unroll
             for (int o = 0; o < 2; ++o)
               *reinterpret_cast<f16x8*>(mine + j * 2048 + o * 1024 + lane * 16) = t.q[s][j][o];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < SB; ++j)
 #pragma unroll
             for (int st = 0; st < 2; ++st) t.q[s][j][st] = tr_run(mine + j * 2048, st, lane);
         }
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < SB; ++i) {
             if constexpr (kTr) {
               // the diagonal's part: diag(e) times x's own rows
               if (kb == rb0 + i) {
@@ -789,18 +791,18 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) e[k] = k == at ? static_cast<_Float16>(e16) : static_cast<_Float16>(0.0f);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < SB; ++j)
                   acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(t.q[s][j][st], e, acc[i][j], 0, 0, 0);
               }
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < SB; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(t.q[s][j][st], t.p[s][i][st], acc[i][j], 0, 0, 0);
           }
       }
     }
   };
-  constexpr int kStep = kSWaves * kSAhead;
+  constexpr int kStep = kSWaves * kAhead;
   Set s0, s1;
   load(wave, s0);
   for (int base = wave; base < nkb; base += 2 * kStep) {
@@ -811,9 +813,10 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   }
 
   // ---- this wave's part of the output: rows of row block i, columns 16 p .. of column block j
-  const int unit = wave >> 1, p = wave & 1, ui = unit >> 1, uj = unit & 1;
+  const int unit = SB == 2 ? wave >> 1 : 0, p = wave & 1, ui = unit >> 1, uj = unit & 1;
+  const bool finishes = wave < 2 * kAcc;                  // (of one block, two waves finish a half each)
   const int rb = rb0 + ui, cb = cb0 + uj;
-  const bool inside = rb < g.mb && cb < g.nb;
+  const bool inside = finishes && rb < g.mb && cb < g.nb;
   const size_t o16 = static_cast<size_t>(2 * g.nb);
   const size_t blk = ((static_cast<size_t>(min(rb, g.mb - 1)) * o16 + 2 * min(cb, g.nb - 1) + p) * 1024 + run[p]) / 2;
   f16x8 ea{}, eb{};
@@ -833,12 +836,12 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   __syncthreads();                                    // x's blocks have been read
   auto exchange = [&](bool store, int slot) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < kAcc; ++b)
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        float* at = red + (slot * 64 + b * 16 + k) * 64 + lane;
-        if (store) *at = acc[b >> 1][b & 1][k];
-        else acc[b >> 1][b & 1][k] += *at;
+        float* at = red + ((slot * kAcc + b) * 16 + k) * 64 + lane;
+        if (store) *at = acc[b / SB][b % SB][k];
+        else acc[b / SB][b % SB][k] += *at;
       }
   };
   if (wave >= kHalf) exchange(true, wave - kHalf);
@@ -853,7 +856,7 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   for (int k = 0; k < 8; ++k) {
     c[k] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kHalf; ++w) c[k] += red[(w * 64 + unit * 16 + 8 * p + k) * 64 + lane];
+    for (int w = 0; w < kHalf; ++w) c[k] += red[((w * kAcc + unit) * 16 + 8 * p + k) * 64 + lane];
   }
   gather_columns(c, v);
   finish<MODE>(v, ea, eb, dpi, dq, jb);
@@ -864,7 +867,7 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
       if (inside) jb.dout[static_cast<size_t>(mat) * g.d_stride + 32 * rb + r] = d;
     }
   }
-  unsigned char* flip = smem + kHalf * 16384 + unit * 2048;
+  unsigned char* flip = smem + sizeof(smem) - kAcc * 2048 + unit * 2048;
   if constexpr (!kOut) {
     const f16x8 w = to_f16(v);
     if (inside) {
@@ -875,7 +878,7 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
     }
     if constexpr (kSym) {
       if (rb0 != cb0) {                               // the mirror image
-        *reinterpret_cast<f16x8*>(flip + p * 1024 + run[p]) = w;
+        if (finishes) *reinterpret_cast<f16x8*>(flip + p * 1024 + run[p]) = w;
         __syncthreads();
         const f16x8 t = tr_run(flip, p, lane);
         if (inside)
@@ -886,17 +889,20 @@ __global__ __launch_bounds__(kSThreads) void orth_small_kernel(OrthArgs g) {
   } else {
     u32x4 o = to_bf16(v, g.scale / kSX);
     if (g.tall) {
-      *reinterpret_cast<u32x4*>(flip + p * 1024 + run[p]) = o;
+      if (finishes) *reinterpret_cast<u32x4*>(flip + p * 1024 + run[p]) = o;
       __syncthreads();
       o = __builtin_bit_cast(u32x4, tr_run(flip, p, lane));
     }
-    store_user(g, mat, 32 * (g.tall ? cb : rb) + r, 32 * (g.tall ? rb : cb) + 16 * p + 8 * h, o);
+    if (finishes)
+      store_user(g, mat, 32 * (g.tall ? cb : rb) + r, 32 * (g.tall ? rb : cb) + 16 * p + 8 * h, o);
   }
 }
 
 // ------------------------------------------------------------------ input
 constexpr int kSumThreads = 256;
-constexpr int kSumElems = 16384;       // elements per workgroup of the sums
+// Elements per workgroup of the sums: 8 vectors a thread, fewer for small
+// inputs (as long as a matrix has at most 256 partial sums).
+constexpr int kSumFew = 8 * kSumThreads, kSumMany = 64 * kSumThreads;
 
 template <typename T>
 __device__ __forceinline__ float load_elem(const T* p) {
@@ -945,11 +951,12 @@ __device__ __forceinline__ double inverse_norm(double s, float eps) {
 // reach 1e38, and their squares would leave fp32.
 template <typename T>
 __global__ __launch_bounds__(kSumThreads) void orth_sums_kernel(const T* g, float* mom, float mu, bool nesterov,
-                                                                int64_t elems, int parts, double* sums) {
+                                                                int64_t elems, int each, int parts,
+                                                                double* sums) {
   __shared__ double red[kSumThreads / 64];
   const size_t base = static_cast<size_t>(blockIdx.y) * elems;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kSumElems;
-  const int64_t end = min(first + kSumElems, elems);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * each;
+  const int64_t end = min(first + each, elems);
   double s = 0.0;
   auto one = [&](float gv, float& m) {
     float u = gv;
@@ -997,7 +1004,7 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
                                                         const double* sums, int nb, _Float16* hi, _Float16* lo,
                                                         int64_t x_stride) {
   __shared__ __attribute__((aligned(16))) unsigned char buf[2][32 * kPackCols * 2];
-  __shared__ double s_inv;
+  __shared__ double s_sum[4];
   const int mat = blockIdx.z, rb = blockIdx.y, c0 = blockIdx.x * kPackCols;
   const int tid = threadIdx.x;
   const size_t base = static_cast<size_t>(mat) * rows * cols;
@@ -1031,15 +1038,13 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
       }
     }
   }
-  if (tid < 64) {
-    double s = 0.0;
-    for (int i = tid; i < parts; i += 64) s += sums[static_cast<size_t>(mat) * parts + i];
+  double s = 0.0;
+  for (int i = tid; i < parts; i += 256) s += sums[static_cast<size_t>(mat) * parts + i];
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-    if (tid == 0) s_inv = inverse_norm(s, eps);
-  }
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  if ((tid & 63) == 0) s_sum[tid >> 6] = s;
   __syncthreads();
-  const double inv = s_inv;
+  const double inv = inverse_norm((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]), eps);
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
     const int i = tid + 256 * k;
@@ -1474,7 +1479,7 @@ bool resident(int m, int n) {
 
 // -------------------------------------------------------------- workspace
 struct OrthPlan {
-  int m, n, mp, np, parts;
+  int m, n, mp, np, each, parts;
   size_t x_elems, s_elems;             // elements of one x and one symmetric matrix
   size_t off_x[4], off_s[4], off_d[4], off_sums, bytes;
 };
@@ -1489,7 +1494,10 @@ OrthPlan plan_of(int64_t count, int rows, int cols) {
   p.mp = pad(p.m);
   p.np = pad(p.n);
   const int64_t elems = static_cast<int64_t>(rows) * cols;
-  p.parts = static_cast<int>((elems + kSumElems - 1) / kSumElems);
+  p.each = kSumMany;
+  if (count * elems <= int64_t{2048} * kSumFew)
+    p.each = static_cast<int>((elems / 256 + kSumFew) / kSumFew) * kSumFew;
+  p.parts = static_cast<int>((elems + p.each - 1) / p.each);
   p.x_elems = static_cast<size_t>(p.mp) * p.np;
   p.s_elems = static_cast<size_t>(p.mp) * p.mp;
   size_t at = 0;
@@ -1506,8 +1514,11 @@ OrthPlan plan_of(int64_t count, int rows, int cols) {
   return p;
 }
 
-// whether the first two steps are taken together
-bool paired(int m, int n, int steps) { return steps >= 2 && m >= 256 && 2 * n >= 3 * m; }
+// Whether the first two steps are taken together: a launch more, so not where
+// the launches are what counts (1 matrix of 256 x 2048: 36.5 us against 34.6).
+bool paired(int64_t count, int m, int n, int steps) {
+  return steps >= 2 && m >= 256 && 2 * n >= 3 * m && (m >= 512 || count * m * n >= (1 << 24));
+}
 
 template <int WB, int MODE>
 void launch_one(const OrthArgs& a, hipStream_t st) {
@@ -1524,14 +1535,19 @@ void launch_mode(const OrthArgs& a, hipStream_t st) {
     const int64_t mt = (a.mb + blocks - 1) / blocks, nt = (a.nb + blocks - 1) / blocks;
     return (MODE <= kMul ? mt * (mt + 1) / 2 : mt * nt) * a.count;
   };
-  // One round of 64-wide tiles where they fit one (update of 1 matrix of
-  // 256 x 2048: 122 us against 143 with 128-wide ones); 256-wide tiles where
+  // One round of 32- or 64-wide tiles where they fit one (update of 1 matrix of
+  // 256 x 2048: 143 us with 128-wide tiles, 122 with 64-wide ones, 99 with
+  // 32-wide ones for R and Q; of 1024 x 1024: 150 with 64-wide ones, 175 with
+  // 32-wide ones, two rounds); 256-wide tiles where
   // there are enough of them and K pays for their long epilogue (256 matrices
   // of 1024 x 2048: 12.1 ms against 14.5; 32 of 512 x 2048, K = 512: products
   // with x 82 us against 72 with 128-wide ones).
-  if (tiles_of(2) <= 256) {
+  if (tiles_of(1) <= 256) {
+    const int64_t tiles = tiles_of(1);
+    orth_small_kernel<1, MODE><<<static_cast<int>((tiles + 7) / 8 * 8), kSThreads, 0, st>>>(a);
+  } else if (tiles_of(2) <= 256) {
     const int64_t tiles = tiles_of(2);
-    orth_small_kernel<MODE><<<static_cast<int>((tiles + 7) / 8 * 8), kSThreads, 0, st>>>(a);
+    orth_small_kernel<2, MODE><<<static_cast<int>((tiles + 7) / 8 * 8), kSThreads, 0, st>>>(a);
   } else if (tiles_of(8) >= 192 && a.mb >= 8 && (MODE <= kMul || a.K >= 1024)) {
     launch_one<4, MODE>(a, st);
   } else {
@@ -1573,12 +1589,12 @@ hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, co
   const dim3 gs(p.parts, n), gp((p.np + kPackCols - 1) / kPackCols, p.mp / 32, n);
   if (bf16) {
     const bf16_t* gb = static_cast<const bf16_t*>(g);
-    orth_sums_kernel<bf16_t><<<gs, kSumThreads, 0, st>>>(gb, mom, mu, nesterov, elems, p.parts, sums);
+    orth_sums_kernel<bf16_t><<<gs, kSumThreads, 0, st>>>(gb, mom, mu, nesterov, elems, p.each, p.parts, sums);
     orth_pack_kernel<bf16_t><<<gp, 256, 0, st>>>(gb, mom, mu, nesterov, rows, cols, tall, eps, p.parts, sums,
                                                  p.np / 32, X[0], X[1], p.x_elems);
   } else {
     const float* gf = static_cast<const float*>(g);
-    orth_sums_kernel<float><<<gs, kSumThreads, 0, st>>>(gf, mom, mu, nesterov, elems, p.parts, sums);
+    orth_sums_kernel<float><<<gs, kSumThreads, 0, st>>>(gf, mom, mu, nesterov, elems, p.each, p.parts, sums);
     orth_pack_kernel<float><<<gp, 256, 0, st>>>(gf, mom, mu, nesterov, rows, cols, tall, eps, p.parts, sums,
                                                 p.np / 32, X[0], X[1], p.x_elems);
   }
@@ -1638,7 +1654,7 @@ hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, co
   };
 
   int left = steps;
-  if (paired(p.m, p.n, steps)) {
+  if (paired(count, p.m, p.n, steps)) {
     gram();
     poly(U);                                    // Q1
     mul(product(U, kSQ, R, kSX, T, kSX));       // T = Q1 R
