@@ -653,7 +653,9 @@ def _arg(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Opt
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}: "
                          f"{tuple(shape)} {dtype} on the device of the others is wanted")
-    return _ptr(t)
+    if device < 0 or not t.is_contiguous():
+        _ptr(t)                                        # (raises)
+    return t.data_ptr()
 
 
 def _workspace_arg(t: Optional[torch.Tensor], device: int) -> Optional[int]:
@@ -662,11 +664,14 @@ def _workspace_arg(t: Optional[torch.Tensor], device: int) -> Optional[int]:
     return _ptr(t)
 
 
-def _stream_of(stream, t: torch.Tensor) -> int:
-    """The given stream, or the current one of the tensors' device, which has to be the current device
-    (the library launches on the current device)."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors on {t.device} while cuda:{torch.cuda.current_device()} is current")
+def _stream_on(stream, device: int) -> int:
+    """The given stream, or the current one of CUDA device `device`, which has to be the current device (the
+    library launches on the current device)."""
+    current = torch.cuda.current_device()
+    if device != current:
+        raise ValueError(f"tensors on cuda:{device} while cuda:{current} is current")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(current)
     return _stream(stream)
 
 
@@ -685,7 +690,7 @@ def moe_norm_forward(kind, x, residual, gamma, beta, eps, sum, y, mean, rstd, st
     out_y = _arg(y, shape, dt, dev, "y")
     me, rs = _arg(mean, (rows,), f32, dev, "mean"), _arg(rstd, (rows,), f32, dev, "rstd")
     _check(lib().moe_norm_forward(kind, rows, cols, _elem(x, "x"), _ptr(x), res, ga, be, eps, out_sum, out_y, me, rs,
-                                  _stream_of(stream, x)), "moe_norm_forward")
+                                  _stream_on(stream, dev)), "moe_norm_forward")
 
 
 def moe_norm_backward(kind, dy, x, gamma, mean, rstd, dsum, dx, dgamma, dbeta, workspace, stream=None):
@@ -699,7 +704,7 @@ def moe_norm_backward(kind, dy, x, gamma, mean, rstd, dsum, dx, dgamma, dbeta, w
         _arg(gamma, (cols,), f32, dev, "gamma"), _arg(mean, (rows,), f32, dev, "mean"),
         _arg(rstd, (rows,), f32, dev, "rstd"), _arg(dsum, shape, dt, dev, "dsum"), _arg(dx, shape, dt, dev, "dx"),
         _arg(dgamma, (cols,), f32, dev, "dgamma"), _arg(dbeta, (cols,), f32, dev, "dbeta"),
-        _workspace_arg(workspace, dev), _nbytes(workspace), _stream_of(stream, x)), "moe_norm_backward")
+        _workspace_arg(workspace, dev), _nbytes(workspace), _stream_on(stream, dev)), "moe_norm_backward")
 
 
 def moe_orthogonalize_workspace_bytes(count, rows, cols) -> int:
@@ -717,4 +722,4 @@ def moe_orthogonalize(g, momentum, mu, nesterov, steps, eps, scale, out, workspa
     mo, to = _arg(momentum, shape, torch.float32, dev, "momentum"), _arg(out, shape, torch.bfloat16, dev, "out")
     _check(lib().moe_orthogonalize(
         count, rows, cols, _elem(g, "g"), _ptr(g), mo, mu, int(bool(nesterov)), steps, eps, scale, to,
-        _workspace_arg(workspace, dev), _nbytes(workspace), _stream_of(stream, g)), "moe_orthogonalize")
+        _workspace_arg(workspace, dev), _nbytes(workspace), _stream_on(stream, dev)), "moe_orthogonalize")
