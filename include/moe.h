@@ -471,15 +471,17 @@ size_t moe_norm_workspace_bytes(int64_t rows, int32_t cols);
  *   workspace  >= moe_norm_workspace_bytes bytes (not needed without dgamma and
  *              dbeta)
  * The sums over rows run in a fixed order: the results are bit-reproducible.
- * rows == 0 writes zeros to dgamma and dbeta. */
+ * The workspace holds nothing between calls; calls and captured graphs that may
+ * run at the same time need one each.  rows == 0 writes zeros to dgamma and dbeta. */
 int moe_norm_backward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, const void* dy,
                       const void* x, const float* gamma, const float* mean, const float* rstd,
                       const void* dsum, void* dx, float* dgamma, float* dbeta, void* workspace,
                       size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace moe_orthogonalize needs (0 for sizes it rejects, and for
- * empty ones): about 8 to 18 bytes an element of g, more for square and small
- * matrices. */
+ * empty ones): 8 bytes an element of g (padded) and 8 bytes an element of a
+ * symmetric matrix on its shorter side; 256 bytes for matrices that one
+ * workgroup holds. */
 size_t moe_orthogonalize_workspace_bytes(int64_t count, int32_t rows, int32_t cols);
 
 /* Orthogonalised update of `count` weight matrices, the direction of the Muon
@@ -502,7 +504,10 @@ size_t moe_orthogonalize_workspace_bytes(int64_t count, int32_t rows, int32_t co
  * A zero matrix gives zeros; an infinity or a NaN in u makes that matrix's
  * output NaN and touches no other.  Products run on fp16 operands with fp32
  * accumulation, held finer where the result needs it (error against 64 bits
- * about the rounding of the bf16 output).
+ * about the rounding of the bf16 output).  Bit-reproducible for the same sizes
+ * and count; a matrix's bits may depend on how many are given with it.
+ * The workspace holds nothing between calls; calls and captured graphs that may
+ * run at the same time need one each.
  * rows, cols <= 65536, rows * cols < 2^30, count <= 65535, count * rows * cols <
  * 2^36 (else MOE_ERR_UNSUPPORTED). */
 int moe_orthogonalize(int64_t count, int32_t rows, int32_t cols, int32_t dtype, const void* g,

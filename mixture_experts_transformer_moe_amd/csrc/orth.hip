@@ -1080,7 +1080,7 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
 
 // ------------------------------------------------------------ small matrices
 // A whole update in one workgroup, for matrices whose x fits its LDS: the
-// launches of the general path (16 of about 5 us) would be most of the time.
+// launches of the general path (17 of about 5 us) would be most of the time.
 //   * x stays in registers, in fp32 and in accumulator order: wave w owns the
 //     blocks w, w + 8, ... (row block t mod MB, column block t / MB); its fp16
 //     copy, the products' operand, is in LDS in blocks as above;
