@@ -467,7 +467,7 @@ size_t moe_norm_workspace_bytes(int64_t rows, int32_t cols);
  *              other way (the residual stream); dx is then the gradient of both
  *              x and residual
  *   dx         [rows, cols] elem out; may be dy, x or dsum itself
- *   dgamma, dbeta [cols] fp32 out; either may be NULL
+ *   dgamma, dbeta [cols] fp32 out; either may be NULL; no overlap beside dx's
  *   workspace  >= moe_norm_workspace_bytes bytes (not needed without dgamma and
  *              dbeta)
  * The sums over rows run in a fixed order: the results are bit-reproducible.

@@ -38,6 +38,29 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
       return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p);            \
   } while (0)
 
+// do [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && p < q + nb && q < p + na;
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// whether an output meets another output, or an input where that is not allowed
+template <int O, int I>
+bool outputs_meet(const Span (&out)[O], const Span (&in)[I]) {
+  for (int i = 0; i < O; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+    for (const Span& s : in)
+      if (overlap(out[i].p, out[i].n, s.p, s.n)) return true;
+  }
+  return false;
+}
+
 // Shape checks common to every entry point.
 int check_shape(const moe_shape* s) {
   if (s == nullptr) return fail(MOE_ERR_INVALID_ARG, "shape is NULL");
@@ -633,12 +656,6 @@ int check_orth(int64_t count, int32_t rows, int32_t cols) {
   return MOE_OK;
 }
 
-// do [a, a + na) and [b, b + nb) share a byte
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && p < q + nb && q < p + na;
-}
-
 }  // namespace
 
 int moe_norm_forward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, const void* x,
@@ -664,8 +681,15 @@ int moe_norm_forward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, co
     for (const void* in : {x, residual})
       if (out != in && overlap(out, bytes, in, bytes))
         return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input without being it");
+  const size_t row = static_cast<size_t>(rows) * 4, col = static_cast<size_t>(cols) * 4;
+  float* mean_out = layer ? mean : nullptr;
+  const Span stats[] = {{mean_out, row}, {rstd, row}}, all[] = {{x, bytes}, {residual, bytes}, {sum, bytes},
+                                                               {y, bytes}, {gamma, col}, {beta, col}};
+  const Span rows_out[] = {{sum, bytes}, {y, bytes}}, weights[] = {{gamma, col}, {beta, col}};
+  if (outputs_meet(stats, all) || outputs_meet(rows_out, weights))
+    return fail(MOE_ERR_INVALID_ARG, "sum, y, mean, rstd and the inputs overlap");
   return launched(moe::launch_norm_forward(layer, rows, cols, bf16, x, residual, gamma, beta, eps, sum, y,
-                                           layer ? mean : nullptr, rstd, as_stream(stream)));
+                                           mean_out, rstd, as_stream(stream)));
 }
 
 size_t moe_norm_workspace_bytes(int64_t rows, int32_t cols) {
@@ -693,8 +717,17 @@ int moe_norm_backward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, c
     for (const void* in : {dy, x, dsum})
       if (dx != in && overlap(dx, bytes, in, bytes))
         return fail(MOE_ERR_INVALID_ARG, "dx overlaps an input without being it");
+    const size_t row = static_cast<size_t>(rows) * 4, col = static_cast<size_t>(cols) * 4;
+    const float* mean_in = layer ? mean : nullptr;
+    const Span rows_out[] = {{dx, bytes}}, weights[] = {{gamma, col}, {mean_in, row}, {rstd, row}};
+    if (outputs_meet(rows_out, weights)) return fail(MOE_ERR_INVALID_ARG, "dx and the inputs overlap");
     if (dgamma != nullptr || dbeta != nullptr) {
-      if (int r = check_workspace(workspace, workspace_bytes, moe::norm_workspace_bytes(rows, cols))) return r;
+      const size_t need = moe::norm_workspace_bytes(rows, cols);
+      if (int r = check_workspace(workspace, workspace_bytes, need)) return r;
+      const Span sums[] = {{dgamma, col}, {dbeta, col}, {workspace, need}};
+      const Span all[] = {{dx, bytes}, {dy, bytes}, {x, bytes}, {dsum, bytes}, {gamma, col}, {mean_in, row}, {rstd, row}};
+      if (outputs_meet(sums, all))
+        return fail(MOE_ERR_INVALID_ARG, "dgamma, dbeta, workspace and the other arguments overlap");
     }
   }
   return launched(moe::launch_norm_backward(layer, rows, cols, bf16, dy, x, gamma, mean, rstd, dsum, dx, dgamma,

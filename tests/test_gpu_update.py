@@ -179,6 +179,24 @@ def test_norm_in_place_and_no_rows():
     assert (dg == 0).all() and (db == 0).all()
 
 
+def test_norm_past_two_to_the_31_elements():
+    # the last rows alone give the same bits (rows do not depend on each other)
+    say("norm 140000x16384 bf16")
+    rows, cols, last = 140000, 16384, 5
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    y, mean, rstd = torch.empty_like(x), f32(rows), f32(rows)
+    M.moe_norm_forward(M.MOE_NORM_LAYER, x, None, None, None, 1e-6, None, y, mean, rstd)
+    x1 = x[-last:].clone()
+    y1, mean1, rstd1 = torch.empty_like(x1), f32(last), f32(last)
+    M.moe_norm_forward(M.MOE_NORM_LAYER, x1, None, None, None, 1e-6, None, y1, mean1, rstd1)
+    assert torch.equal(y[-last:], y1) and torch.equal(mean[-last:], mean1) and torch.equal(rstd[-last:], rstd1)
+    dx, dx1 = torch.empty_like(x), torch.empty_like(x1)
+    M.moe_norm_backward(M.MOE_NORM_LAYER, y, x, None, mean, rstd, None, dx, None, None, None)
+    M.moe_norm_backward(M.MOE_NORM_LAYER, y1, x1, None, mean1, rstd1, None, dx1, None, None, None)
+    torch.cuda.synchronize()
+    assert torch.equal(dx[-last:], dx1)
+
+
 # ---------------------------------------------------------------- the update
 
 def gradient(rng, rows, cols, tokens):
@@ -233,6 +251,39 @@ def test_orthogonalize_many_tiles(count, rows, cols):
     out = orth(g)
     for i in (0, 1, count // 2, count - 1):
         check_update(out[i], U.orthogonalize(to_f64(g[i])), f"{i}")
+
+
+def test_orthogonalize_past_two_to_the_31_elements():
+    # (24 GB of workspace; the last matrices against the oracle)
+    count, rows, cols = 2100, 512, 2048
+    say(f"orthogonalize {count}x{rows}x{cols} bf16")
+    g = torch.empty(count, rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    out = orth(g)
+    for i in (0, count - 1):
+        check_update(out[i], U.orthogonalize(to_f64(g[i])), f"{i}")
+
+
+@pytest.mark.parametrize("rows,cols", [(4000, 20000), (20000, 4000)])
+def test_orthogonalize_large_matrix(rows, cols):
+    # against the formula in 64 bits on the device (Q commutes with R, so R' = Q R Q)
+    say(f"orthogonalize {rows}x{cols} f32")
+    g = torch.empty(rows, cols, device="cuda").normal_()
+    out = orth(g)
+    x = out.float() if rows < cols else out.float().t().contiguous()
+    u = g if rows < cols else g.t().contiguous()
+    want = u.double() / u.double().norm()
+    r = want @ want.t().contiguous()
+    one = torch.eye(r.shape[0], dtype=torch.float64, device="cuda")
+    m = one
+    for _ in range(5):
+        q = 3.4445 * one - 4.7750 * r + 2.0315 * (r @ r)
+        m = q @ m
+        r = q @ r @ q
+    ref = m @ want
+    torch.cuda.synchronize()
+    err = (x.double() - ref).norm() / ref.norm()
+    say(f"rel {float(err):.2e}")
+    assert err <= 2 * b16
 
 
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 8])

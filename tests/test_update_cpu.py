@@ -96,6 +96,9 @@ def _fwd(L, kind=1, rows=4, cols=64, dtype=1, x=P(1), res=None, gamma=P(2), beta
     (dict(sum=P(5)), binding.MOE_ERR_INVALID_ARG, b"sum"),
     (dict(res=P(5), sum=P(3)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
     (dict(y=ctypes.c_void_p((1 << 32) + 16)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(rstd=P(1)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(kind=0, mean=P(9), rstd=P(9)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(gamma=P(7), y=P(7)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
 ])
 def test_norm_forward_refusals(L, kw, status, word):
     assert _fwd(L, **kw) == status
@@ -125,6 +128,11 @@ def _bwd(L, kind=0, rows=4, cols=64, dtype=1, dy=P(1), x=P(2), gamma=P(3), mean=
     (dict(ws=None), binding.MOE_ERR_WORKSPACE, b"workspace"),
     (dict(nbytes=8), binding.MOE_ERR_WORKSPACE, b"workspace"),
     (dict(dx=ctypes.c_void_p((2 << 32) + 64)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(dx=P(5)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(dbeta=P(7)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(dgamma=P(3)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(ws=P(1)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
+    (dict(ws=P(8)), binding.MOE_ERR_INVALID_ARG, b"overlap"),
 ])
 def test_norm_backward_refusals(L, kw, status, word):
     assert _bwd(L, **kw) == status
