@@ -946,6 +946,21 @@ __device__ __forceinline__ double inverse_norm(double s, float eps) {
   return s < 1.0 / 0.0 ? (norm > 0.0 ? kSX / norm : 0.0) : 0.0 / 0.0;
 }
 
+// v f as ldexp(v, e) * m: in fp32, for a factor f outside its range (|v f| is
+// at most kSX; m is f's mantissa rounded to fp32)
+struct Factor {
+  float m;
+  int e;
+};
+
+__device__ __forceinline__ Factor factor_of(double f) {
+  Factor r;
+  r.m = static_cast<float>(frexp(f, &r.e));
+  return r;
+}
+
+__device__ __forceinline__ float scaled(float v, const Factor& f) { return ldexpf(v, f.e) * f.m; }
+
 // Sums of squares of the update u = g (or, with momentum, M <- mu M + g and
 // u = g + mu M or M), 8 elements a thread at a time.  In 64 bits: bf16 values
 // reach 1e38, and their squares would leave fp32.
@@ -1044,7 +1059,7 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
   for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
   if ((tid & 63) == 0) s_sum[tid >> 6] = s;
   __syncthreads();
-  const double inv = inverse_norm((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]), eps);
+  const Factor inv = factor_of(inverse_norm((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]), eps));
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
     const int i = tid + 256 * k;
@@ -1052,7 +1067,7 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
     f16x8 a, b;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float v = static_cast<float>(u[k][e] * inv);
+      const float v = scaled(u[k][e], inv);
       a[e] = static_cast<_Float16>(v);
       b[e] = static_cast<_Float16>(v - static_cast<float>(a[e]));
     }
@@ -1179,6 +1194,9 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
     for (int s = 0; s < kResLoads; ++s) {
       const int t = t0 + s;
 #pragma unroll
+      for (int q = 0; q < 16; ++q) x[t][q] = 0.0f;
+      if (opaque(wave + kSWaves * t) >= blocks) continue;
+#pragma unroll
       for (int k = 0; k < 2; ++k) {
         int ur, uc;
         const bool in = place(t, k, ur, uc);
@@ -1203,14 +1221,24 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
 #pragma unroll
         for (int e = 0; e < 8; ++e) stg[(16 * k + (lane >> 2)) * 33 + 8 * (lane & 3) + e] = v[s][k][e];
       }
-      // register q of a lane: row r, column 8 (q / 4) + 4 h + q mod 4 (blocks
-      // past the matrix are zeros)
+      // register q of a lane: row r, column 8 (q / 4) + 4 h + q mod 4
+      float big = 0.0f;
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         const int c = 8 * (q >> 2) + 4 * h + (q & 3);
         x[t][q] = tall ? stg[c * 33 + r] : stg[r * 33 + c];
-        ss = fma(static_cast<double>(x[t][q]), static_cast<double>(x[t][q]), ss);
+        big = fmaxf(big, fabsf(x[t][q]));
       }
+      // a block's squares in fp32, relative to its largest element
+      int e;
+      frexpf(big, &e);
+      float s2 = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const float y = ldexpf(x[t][q], -e);
+        s2 = fmaf(y, y, s2);
+      }
+      ss += ldexp(static_cast<double>(s2), 2 * e);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -1221,14 +1249,12 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
   ss = 0.0;
 #pragma unroll
   for (int w = 0; w < kSWaves; ++w) ss += red[w];
-  const double inv = inverse_norm(ss, eps);
+  const Factor inv = factor_of(inverse_norm(ss, eps));
 #pragma unroll
   for (int t = 0; t < kResBlocks; ++t) {
+    if (opaque(wave + kSWaves * t) >= blocks) continue;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      asm volatile("" : "+v"(x[t][q]));               // (or the conversions to 64 bits above would be kept)
-      x[t][q] = static_cast<float>(x[t][q] * inv);
-    }
+    for (int q = 0; q < 16; ++q) x[t][q] = scaled(x[t][q], inv);
     __builtin_amdgcn_sched_barrier(0);
   }
 
