@@ -1437,20 +1437,29 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
       }
     }
     __syncthreads();
-    // ---- x <- Q x
+    // ---- x <- Q x (a wave's blocks share their row, and with it Q's operands,
+    // where its stride through the blocks keeps the row)
+    constexpr bool kOneRow = kSWaves % MB == 0;
+    f16x8 qa[2 * MB];
+    auto load_q = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+      for (int z = 0; z < 2 * MB; ++z)
+        qa[z] = *reinterpret_cast<const f16x8*>(ms + (i * 2 * MB + z) * 1024 + run[z & 1]);
+    };
+    if constexpr (kOneRow) load_q(wave % MB);
 #pragma unroll
     for (int t = 0; t < kResBlocks; ++t) {
       const int b = opaque(wave + kSWaves * t);
       if (b < blocks) {
         const int i = b % MB, j = b / MB;
+        if constexpr (!kOneRow) load_q(i);
         f32x16 y = f32x16{0.f};
 #pragma unroll
         for (int kb = 0; kb < MB; ++kb)
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const f16x8 a = *reinterpret_cast<const f16x8*>(ms + (i * 2 * MB + 2 * kb + st) * 1024 + run[st]);
-            y = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_run(xs + (kb * 2 * nb + 2 * j) * 1024, st, lane), a, y, 0, 0, 0);
-          }
+          for (int st = 0; st < 2; ++st)
+            y = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_run(xs + (kb * 2 * nb + 2 * j) * 1024, st, lane),
+                                                       qa[2 * kb + st], y, 0, 0, 0);
         const float di = qd[32 * i + r];
 #pragma unroll
         for (int q = 0; q < 16; ++q) x[t][q] = fmaf(di, x[t][q], y[q] * (1.0f / kSQ));
