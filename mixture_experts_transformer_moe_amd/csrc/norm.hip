@@ -30,6 +30,8 @@
 namespace moe {
 namespace {
 
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
 template <typename T>
 struct Vec;
 template <>
@@ -44,12 +46,25 @@ struct Vec<float> {
 };
 
 // the vector of a row that starts at element c (c < cols), as it is stored;
-// elements past the row's end are 0
+// elements past the row's end are 0.  A ragged last vector comes out of the one
+// that ends with the row, shifted (element by element: 32768 x 100 in bf16, the
+// backward pass, 26.8 us instead of 19.9).
 template <typename T>
 __device__ __forceinline__ u32x4 load_raw(const T* row, int c, int cols) {
   constexpr int N = Vec<T>::kN;
-  if (c + N <= cols) return *reinterpret_cast<const typename Vec<T>::raw*>(row + c);
+  typedef typename Vec<T>::raw raw;
+  if (c + N <= cols) return *reinterpret_cast<const raw*>(row + c);
   u32x4 w = {0, 0, 0, 0};
+  if (cols >= N) {
+    w = *reinterpret_cast<const raw*>(row + cols - N);
+    const int s = c + N - cols;                       // elements to drop
+    const int words = N == 8 ? s >> 1 : s;
+    if (words & 1) w = u32x4{w[1], w[2], w[3], 0};
+    if (words & 2) w = u32x4{w[2], w[3], 0, 0};
+    if (N == 8 && (s & 1))
+      w = u32x4{(w[0] >> 16) | (w[1] << 16), (w[1] >> 16) | (w[2] << 16), (w[2] >> 16) | (w[3] << 16), w[3] >> 16};
+    return w;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (c + i < cols) {
@@ -85,12 +100,36 @@ __device__ __forceinline__ void store_vec(T* row, int c, int cols, const float (
     }
     *reinterpret_cast<typename Vec<T>::raw*>(row + c) = w;
   } else {
+    // pieces of 4, 2 and 1 elements
+    u32x4 w;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (c + i < cols) {
-        if constexpr (N == 8) row[c + i] = f32_to_bf16(v[i]);
-        else row[c + i] = v[i];
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (N == 8) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      else w[i] = __float_as_uint(v[i]);
+    }
+    const int n = cols - c;
+    T* p = row + c;
+    typedef uint32_t two __attribute__((ext_vector_type(2), aligned(2)));
+    typedef uint32_t one __attribute__((aligned(2)));
+    if constexpr (N == 8) {
+      if (n & 4) {
+        *reinterpret_cast<two*>(p) = two{w[0], w[1]};
+        p += 4;
+        w = u32x4{w[2], w[3], 0, 0};
       }
+      if (n & 2) {
+        *reinterpret_cast<one*>(p) = w[0];
+        p += 2;
+        w[0] = w[1];
+      }
+      if (n & 1) *p = static_cast<T>(w[0]);
+    } else {
+      if (n & 2) {
+        *reinterpret_cast<two*>(p) = two{w[0], w[1]};
+        p += 2;
+        w[0] = w[2];
+      }
+      if (n & 1) *p = __uint_as_float(w[0]);
     }
   }
 }
@@ -99,7 +138,20 @@ __device__ __forceinline__ void store_vec(T* row, int c, int cols, const float (
 template <int N>
 __device__ __forceinline__ void load_weight(const float* w, int c, int cols, float fill, float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = w != nullptr && c + i < cols ? w[c + i] : fill;
+  for (int i = 0; i < N; ++i) v[i] = fill;
+  if (w == nullptr || c >= cols) return;
+  if (c + N <= cols) {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      const f32x4 q = *reinterpret_cast<const f32x4u*>(w + c + 4 * k);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * k + i] = q[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < cols) v[i] = w[c + i];
+  }
 }
 
 // sums of K values over the WPR waves of a row's group; every thread gets them
@@ -341,9 +393,15 @@ __global__ __launch_bounds__(threads_of(WPR, true)) void norm_backward_kernel(No
       }
       const int c = (k * kT + t) * N;
       if (grp == 0) {
+        float* p = part + static_cast<size_t>(b) * cols + c;
+        if (c + N <= cols) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (c + i < cols) part[static_cast<size_t>(b) * cols + c + i] = v[i];
+          for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4u*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (c + i < cols) p[i] = v[i];
+        }
       }
     }
 }
