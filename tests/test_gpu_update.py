@@ -133,6 +133,15 @@ def test_norm_backward(rows, cols, kind, dtype):
         assert (db == 7.0).all()
 
 
+# rows that share a wave, ragged ends of every length, three vectors a thread
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1100, 60), (1100, 100), (1027, 250), (1030, 2100), (1030, 4101)] +
+                         [(5, 8 + k) for k in range(1, 8)] + [(1025, 15 + k) for k in range(3)])
+def test_norm_forms(rows, cols, dtype):
+    test_norm_forward(rows, cols, "layer", dtype)
+    test_norm_backward(rows, cols, "layer", dtype)
+
+
 def test_norm_of_constant_and_huge_rows():
     # a constant row has no variance: y = beta; values near fp32's square-root range keep finite statistics
     x = torch.ones(4, 300, device="cuda") * torch.tensor([0.0, 3.0, 1e18, -1e-30], device="cuda")[:, None]
