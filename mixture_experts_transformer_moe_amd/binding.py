@@ -165,6 +165,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 # the current stream's handle without a Stream object around it (2.7 us)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device without the check for initialisation (a device tensor is at hand)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream) -> int:
@@ -667,7 +669,7 @@ def _workspace_arg(t: Optional[torch.Tensor], device: int) -> Optional[int]:
 def _stream_on(stream, device: int) -> int:
     """The given stream, or the current one of CUDA device `device`, which has to be the current device (the
     library launches on the current device)."""
-    current = torch.cuda.current_device()
+    current = _device_now()
     if device != current:
         raise ValueError(f"tensors on cuda:{device} while cuda:{current} is current")
     if stream is None and _raw_stream is not None:
@@ -685,12 +687,17 @@ def moe_norm_forward(kind, x, residual, gamma, beta, eps, sum, y, mean, rstd, st
         raise ValueError("x must be [rows, cols]")
     shape, dt, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
     rows, cols = shape
-    res, out_sum = _arg(residual, shape, dt, dev, "residual"), _arg(sum, shape, dt, dev, "sum")
-    ga, be = _arg(gamma, (cols,), f32, dev, "gamma"), _arg(beta, (cols,), f32, dev, "beta")
+    res = None if residual is None else _arg(residual, shape, dt, dev, "residual")
+    out_sum = None if sum is None else _arg(sum, shape, dt, dev, "sum")
+    ga = None if gamma is None else _arg(gamma, (cols,), f32, dev, "gamma")
+    be = None if beta is None else _arg(beta, (cols,), f32, dev, "beta")
     out_y = _arg(y, shape, dt, dev, "y")
-    me, rs = _arg(mean, (rows,), f32, dev, "mean"), _arg(rstd, (rows,), f32, dev, "rstd")
-    _check(lib().moe_norm_forward(kind, rows, cols, _elem(x, "x"), _ptr(x), res, ga, be, eps, out_sum, out_y, me, rs,
-                                  _stream_on(stream, dev)), "moe_norm_forward")
+    me = None if mean is None else _arg(mean, (rows,), f32, dev, "mean")
+    rs = None if rstd is None else _arg(rstd, (rows,), f32, dev, "rstd")
+    status = lib().moe_norm_forward(kind, rows, cols, _elem(x, "x"), _ptr(x), res, ga, be, eps, out_sum, out_y, me,
+                                    rs, _stream_on(stream, dev))
+    if status:
+        _check(status, "moe_norm_forward")
 
 
 def moe_norm_backward(kind, dy, x, gamma, mean, rstd, dsum, dx, dgamma, dbeta, workspace, stream=None):
