@@ -706,12 +706,16 @@ def moe_norm_backward(kind, dy, x, gamma, mean, rstd, dsum, dx, dgamma, dbeta, w
         raise ValueError("x must be [rows, cols]")
     shape, dt, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
     rows, cols = shape
-    _check(lib().moe_norm_backward(
-        kind, rows, cols, _elem(x, "x"), _arg(dy, shape, dt, dev, "dy"), _ptr(x),
-        _arg(gamma, (cols,), f32, dev, "gamma"), _arg(mean, (rows,), f32, dev, "mean"),
-        _arg(rstd, (rows,), f32, dev, "rstd"), _arg(dsum, shape, dt, dev, "dsum"), _arg(dx, shape, dt, dev, "dx"),
-        _arg(dgamma, (cols,), f32, dev, "dgamma"), _arg(dbeta, (cols,), f32, dev, "dbeta"),
-        _workspace_arg(workspace, dev), _nbytes(workspace), _stream_on(stream, dev)), "moe_norm_backward")
+    ga = None if gamma is None else _arg(gamma, (cols,), f32, dev, "gamma")
+    me = None if mean is None else _arg(mean, (rows,), f32, dev, "mean")
+    ds = None if dsum is None else _arg(dsum, shape, dt, dev, "dsum")
+    dg = None if dgamma is None else _arg(dgamma, (cols,), f32, dev, "dgamma")
+    db = None if dbeta is None else _arg(dbeta, (cols,), f32, dev, "dbeta")
+    status = lib().moe_norm_backward(kind, rows, cols, _elem(x, "x"), _arg(dy, shape, dt, dev, "dy"), _ptr(x), ga, me,
+                                     _arg(rstd, (rows,), f32, dev, "rstd"), ds, _arg(dx, shape, dt, dev, "dx"), dg, db,
+                                     _workspace_arg(workspace, dev), _nbytes(workspace), _stream_on(stream, dev))
+    if status:
+        _check(status, "moe_norm_backward")
 
 
 def moe_orthogonalize_workspace_bytes(count, rows, cols) -> int:

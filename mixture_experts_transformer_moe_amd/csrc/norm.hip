@@ -18,7 +18,8 @@
 //     registers, and in the backward pass so do the column sums of dgamma and
 //     dbeta.  Each workgroup writes its sums once, to the workspace, and a
 //     second kernel adds them in a fixed order: no atomics, the same bits on
-//     every call.
+//     every call.  Of few rows, workgroups of their own sum the columns in the
+//     same launch (dgamma and dbeta need no sum over a row).
 //   * Rows of any width: the vectors are loaded from wherever the row starts
 //     (global loads take any element alignment); a last vector that is not
 //     whole is cut out of the one that ends with the row.
@@ -197,6 +198,9 @@ struct NormArgs {
   void* sum;
   void* y;                   // forward: y; backward: dx
   float* part;               // backward: [workgroups][2][cols] (or [1] without dbeta)
+  float* dgamma;             // kOwnSums
+  float* dbeta;
+  int row_blocks;            // backward: workgroups that walk the rows
   int64_t rows;
   int cols;
   int layer;
@@ -281,8 +285,52 @@ __global__ __launch_bounds__(threads_of(TPR, false)) void norm_forward_kernel(No
   }
 }
 
-template <typename T, int CH, int TPR, bool BETA>
+// What a backward launch does beside dx: the column sums of dgamma, of dgamma
+// and dbeta, or all of both by workgroups of their own.
+enum { kSumGamma = 0, kSumBoth = 1, kOwnSums = 2 };
+
+template <typename T>
+__device__ __forceinline__ float elem(const void* p, size_t i) {
+  if constexpr (sizeof(T) == 2) return bf16_to_f32(static_cast<const T*>(p)[i]);
+  else return static_cast<const T*>(p)[i];
+}
+
+// dgamma and dbeta of THREADS / 32 columns: 32 slices of the rows, then the
+// slices, both in a fixed order.
+template <typename T, int THREADS>
+__device__ __forceinline__ void column_sums(const NormArgs& a, int block) {
+  constexpr int kSlices = 32, kCols = THREADS / kSlices;
+  __shared__ float red[2][THREADS];
+  const int c = block * kCols + threadIdx.x % kCols, sl = threadIdx.x / kCols;
+  float g = 0.0f, b = 0.0f;
+  if (c < a.cols) {
+#pragma unroll 8
+    for (int r = sl; r < static_cast<int>(a.rows); r += kSlices) {
+      const size_t at = static_cast<size_t>(r) * a.cols + c;
+      const float dy = elem<T>(a.dy, at), x = elem<T>(a.x, at);
+      g = fmaf(dy, (x - (a.layer ? a.mean[r] : 0.0f)) * a.rstd[r], g);
+      b += dy;
+    }
+  }
+  red[0][threadIdx.x] = g;
+  red[1][threadIdx.x] = b;
+  __syncthreads();
+  if (sl < 2 && c < a.cols) {                       // the first slice joins dgamma, the second dbeta
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSlices; ++i) s += red[sl][i * kCols + threadIdx.x % kCols];
+    float* out = sl ? a.dbeta : a.dgamma;
+    if (out != nullptr) out[c] = s;
+  }
+}
+
+template <typename T, int CH, int TPR, int SUMS>
 __global__ __launch_bounds__(threads_of(TPR, true)) void norm_backward_kernel(NormArgs a) {
+  constexpr bool BETA = SUMS == kSumBoth;
+  if constexpr (SUMS == kOwnSums) {
+    if (static_cast<int>(blockIdx.x) >= a.row_blocks)
+      return column_sums<T, threads_of(TPR, true)>(a, blockIdx.x - a.row_blocks);
+  }
   constexpr int N = Vec<T>::kN, kT = TPR, kG = groups_of(TPR, true);
   __shared__ float red[TPR > 64 ? 2 * TPR / 64 * kG : 1];
   __shared__ float fold[kG > 1 ? (kG - 1) * kT * N : 1];
@@ -324,7 +372,7 @@ __global__ __launch_bounds__(threads_of(TPR, true)) void norm_backward_kernel(No
   };
   // (the widest rows leave no registers for it)
   constexpr bool kEarly = TPR < 1024 || CH == 1;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kG;
+  const int64_t stride = static_cast<int64_t>(a.row_blocks) * kG;
   if (kEarly) load(static_cast<int64_t>(blockIdx.x) * kG, cur);
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kG; row0 < a.rows; row0 += stride) {
     // (dx may be dy, x or dsum itself: other rows than those still to be read)
@@ -340,7 +388,7 @@ __global__ __launch_bounds__(threads_of(TPR, true)) void norm_backward_kernel(No
       for (int i = 0; i < N; ++i) {
         // (past the row's end g is 0, so h adds nothing there)
         h[k][i] = (h[k][i] - cur.mean) * cur.rstd;
-        dg[k][i] = fmaf(g[k][i], h[k][i], dg[k][i]);
+        if constexpr (SUMS != kOwnSums) dg[k][i] = fmaf(g[k][i], h[k][i], dg[k][i]);
         if constexpr (BETA) db[k][i] += g[k][i];
         g[k][i] *= gm[k][i];
         s[0] = fmaf(g[k][i], h[k][i], s[0]);
@@ -365,7 +413,7 @@ __global__ __launch_bounds__(threads_of(TPR, true)) void norm_backward_kernel(No
     }
     if (kEarly) cur = next;
   }
-  if (a.part == nullptr) return;
+  if (SUMS == kOwnSums || a.part == nullptr) return;
   // the workgroup's column sums: its groups' added in order, then stored
   float* part = a.part + static_cast<size_t>(blockIdx.x) * (BETA ? 2 : 1) * cols;
 #pragma unroll
@@ -443,22 +491,23 @@ __global__ __launch_bounds__(kFoldThreads) void norm_fold_kernel(const float* pa
 }
 
 // Vectors per thread (ch) and threads per row (tpr).  Narrow rows share a wave
-// (32768 x 64 in bf16, forward: 6.7 us with 16 threads a row, 16.6 with 64; few
-// rows' column sums then take longer to join: 400 x 64, backward, 7.2 us against
-// 6.5).  Batches of many rows take the fewest waves whose registers leave enough
+// (32768 x 64 in bf16, forward: 6.7 us with 16 threads a row, 16.6 with 64).
+// Batches of many rows take the fewest waves whose registers leave enough
 // of them resident (32768 x 2048 in bf16, forward: 99 us with one vector and 256
 // threads, 124 us with four vectors and 64; 8000 x 4097: 65 us with three and
 // 256, 84 us with one and 1024); few rows are spread over more waves, for
 // latency.
+constexpr int kManyRows = 1024;
+
 struct NormForm {
   int ch, tpr;
 };
 
-NormForm form_of(int64_t rows, int cols, int n, bool backward) {
+NormForm form_of(int64_t rows, int cols, int n) {
   const int vecs = (cols + n - 1) / n;
   auto fits = [&](int ch, int tpr) { return vecs <= ch * tpr; };
-  const bool many = rows >= 1024;
-  for (int tpr = backward && !many ? 64 : 16; tpr <= 64; tpr *= 2)
+  const bool many = rows >= kManyRows;
+  for (int tpr = 16; tpr <= 64; tpr *= 2)
     if (fits(1, tpr)) return {1, tpr};
   if (many && fits(2, 64)) return {2, 64};
   for (int ch = 1; ch <= (many ? 3 : 1); ++ch)
@@ -471,8 +520,8 @@ NormForm form_of(int64_t rows, int cols, int n, bool backward) {
 // Workgroups: what the CUs hold at once by the kernels' registers, and the
 // same number of rows for each (2048 workgroups instead of 1536 for 32768 x
 // 2048, a second round for some: 124 us instead of 99).  A backward pass of few
-// rows takes one a CU, for fewer partial sums (777 x 1023 in fp32: 10.1 us
-// instead of 11.3 with two).
+// rounds takes one a CU, for fewer partial sums (2048 x 2048 in bf16: 13.3 us
+// instead of 15.2 with two).
 int grid_of(int64_t rows, NormForm f, bool backward) {
   const int64_t need = (rows + groups_of(f.tpr, backward) - 1) / groups_of(f.tpr, backward);
   int per_cu = f.tpr == 1024 ? 1 : f.ch == 1 ? 6 : f.ch == 2 ? 4 : 3;
@@ -494,9 +543,13 @@ void launch_fwd(const NormArgs& a, int grid, hipStream_t st) {
 }
 
 template <typename T, int CH, int TPR>
-void launch_bwd(const NormArgs& a, int grid, bool beta, hipStream_t st) {
-  if (beta) norm_backward_kernel<T, CH, TPR, true><<<grid, threads_of(TPR, true), 0, st>>>(a);
-  else norm_backward_kernel<T, CH, TPR, false><<<grid, threads_of(TPR, true), 0, st>>>(a);
+void launch_bwd(const NormArgs& a, int sums, hipStream_t st) {
+  constexpr int kThreads = threads_of(TPR, true);
+  if (sums == kOwnSums)
+    norm_backward_kernel<T, CH, TPR, kOwnSums><<<a.row_blocks + (a.cols + kThreads / 32 - 1) / (kThreads / 32),
+                                                 kThreads, 0, st>>>(a);
+  else if (sums == kSumBoth) norm_backward_kernel<T, CH, TPR, kSumBoth><<<a.row_blocks, kThreads, 0, st>>>(a);
+  else norm_backward_kernel<T, CH, TPR, kSumGamma><<<a.row_blocks, kThreads, 0, st>>>(a);
 }
 
 template <typename T, typename F>
@@ -517,7 +570,7 @@ size_t norm_workspace_bytes(int64_t rows, int cols) {
   // the most workgroups of any form, two sums each
   size_t most = 0;
   for (int n = 4; n <= 8; n += 4) {
-    const NormForm f = form_of(rows, cols, n, true);
+    const NormForm f = form_of(rows, cols, n);
     const size_t b = static_cast<size_t>(grid_of(rows, f, true)) * 2 * cols * sizeof(float);
     most = b > most ? b : most;
   }
@@ -540,7 +593,7 @@ hipError_t launch_norm_forward(bool layer, int64_t rows, int cols, bool bf16, co
   a.cols = cols;
   a.layer = layer;
   a.eps = eps;
-  const NormForm f = form_of(rows, cols, bf16 ? 8 : 4, false);
+  const NormForm f = form_of(rows, cols, bf16 ? 8 : 4);
   const int grid = grid_of(rows, f, false);
   if (bf16) with_form<bf16_t>(f, [&](auto ch, auto w) { launch_fwd<bf16_t, ch(), w()>(a, grid, st); });
   else with_form<float>(f, [&](auto ch, auto w) { launch_fwd<float, ch(), w()>(a, grid, st); });
@@ -561,20 +614,28 @@ hipError_t launch_norm_backward(bool layer, int64_t rows, int cols, bool bf16, c
   a.rows = rows;
   a.cols = cols;
   a.layer = layer;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
   const bool any = dgamma != nullptr || dbeta != nullptr, beta = dbeta != nullptr;
+  // Few rows: dgamma and dbeta by workgroups of their own in the same launch,
+  // which read x and dy once more (out of the caches) instead of writing and
+  // joining partial sums: 777 x 1023 in fp32 7.3 us instead of 9.7, 64 x 4096 in
+  // bf16 3.9 instead of 7.7, 1000 x 2048 11.5 against 11.2, 2500 x 2048 23.3
+  // against 16.0.  Not where dx overwrites what they read.
+  const bool own = any && rows > 0 && rows < kManyRows && dx != dy && dx != x;
   a.part = any ? static_cast<float*>(workspace) : nullptr;
-  int grid = 0;
   if (rows > 0) {
-    const NormForm f = form_of(rows, cols, bf16 ? 8 : 4, true);
-    grid = grid_of(rows, f, true);
-    if (bf16) with_form<bf16_t>(f, [&](auto ch, auto w) { launch_bwd<bf16_t, ch(), w()>(a, grid, beta, st); });
-    else with_form<float>(f, [&](auto ch, auto w) { launch_bwd<float, ch(), w()>(a, grid, beta, st); });
+    const NormForm f = form_of(rows, cols, bf16 ? 8 : 4);
+    a.row_blocks = grid_of(rows, f, true);
+    const int sums = own ? kOwnSums : beta ? kSumBoth : kSumGamma;
+    if (bf16) with_form<bf16_t>(f, [&](auto ch, auto w) { launch_bwd<bf16_t, ch(), w()>(a, sums, st); });
+    else with_form<float>(f, [&](auto ch, auto w) { launch_bwd<float, ch(), w()>(a, sums, st); });
   }
-  if (any) {
+  if (any && !own) {
     auto fold = [&](auto c) {
       constexpr int kCols = decltype(c)::value;
       norm_fold_kernel<kCols><<<dim3((cols + kCols - 1) / kCols, beta ? 2 : 1), kFoldThreads, 0, st>>>(
-          static_cast<const float*>(workspace), grid, beta ? 2 : 1, cols, dgamma, dbeta);
+          static_cast<const float*>(workspace), a.row_blocks, beta ? 2 : 1, cols, dgamma, dbeta);
     };
     // (wide rows: whole 128-byte lines; 4096 x 8192 in bf16 61.8 -> 59.0 us, 4000
     // x 64 8.4 -> 9.3 us)

@@ -182,6 +182,15 @@ def test_norm_in_place_and_no_rows():
     dy2 = dy.clone()
     M.moe_norm_backward(M.MOE_NORM_LAYER, dy2, s, gamma, mean, rstd, r, dy2, None, None, None)
     assert torch.equal(dy2, dx)
+    # in place, the sums' workgroups may not read what dx overwrites
+    for other in (dy.clone(), s.clone()):
+        a, b = (other, s) if torch.equal(other, dy) else (dy, other)
+        dg2, db2 = f32(770), f32(770)
+        M.moe_norm_backward(M.MOE_NORM_LAYER, a, b, gamma, mean, rstd, r, other, dg2, db2, ws)
+        assert torch.equal(other, dx)
+        h = ((s.double() - mean.double()[:, None]) * rstd.double()[:, None]).abs()
+        assert ((dg2 - dg).abs() <= 512 * u32 * ((dy.double().abs() * (h + 1)).sum(0))).all()
+        assert ((db2 - db).abs() <= 512 * u32 * dy.double().abs().sum(0)).all()
     none = torch.empty(0, 770, dtype=torch.bfloat16, device="cuda")
     M.moe_norm_backward(M.MOE_NORM_LAYER, none, none, gamma, f32(0), f32(0), None, none.clone(), dg, db, None)
     torch.cuda.synchronize()
