@@ -466,7 +466,8 @@ size_t moe_norm_workspace_bytes(int64_t rows, int32_t cols);
  *   dsum       [rows, cols] elem or NULL: the gradient that arrives at s on its
  *              other way (the residual stream); dx is then the gradient of both
  *              x and residual
- *   dx         [rows, cols] elem out; may be dy, x or dsum itself
+ *   dx         [rows, cols] elem out; may be dy, x or dsum itself (over dy or x,
+ *              the sums' order, and with it their last bits, can differ)
  *   dgamma, dbeta [cols] fp32 out; either may be NULL; no overlap beside dx's
  *   workspace  >= moe_norm_workspace_bytes bytes (not needed without dgamma and
  *              dbeta)
