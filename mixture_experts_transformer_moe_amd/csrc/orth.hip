@@ -1095,7 +1095,9 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
 
 // ------------------------------------------------------------ small matrices
 // A whole update in one workgroup, for matrices whose x fits its LDS: the
-// launches of the general path (17 of about 5 us) would be most of the time.
+// launches of the general path would be most of the time (1 matrix of 128 x 128:
+// 32 us against 58, of 128 x 400: 58 against 61; 256 of 128 x 128: 34 against
+// 120, of 64 x 1000: 60 against 349).
 //   * x stays in registers, in fp32 and in accumulator order: wave w owns the
 //     blocks w, w + 8, ... (row block t mod MB, column block t / MB); its fp16
 //     copy, the products' operand, is in LDS in blocks as above;
