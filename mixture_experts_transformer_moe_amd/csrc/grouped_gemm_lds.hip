@@ -117,7 +117,7 @@ __device__ __forceinline__ const T* uni(const T* p) {
 // halves of a 64-bit address add, would otherwise be overwritten).
 template <int OFF>
 __device__ __forceinline__ void dma_lds(const unsigned char* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_add_u32 m0, %2, %3\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(voff), "s"(base), "s"(lds), "i"(OFF)
                : "memory", "m0", "scc");
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(kLThreads, 1) void lds_gemm_kernel(GemmArgs g) {
     const unsigned char* base = uni(gath ? reinterpret_cast<const unsigned char*>(t.ids) : dummy);
     const uint32_t voff = gath ? static_cast<uint32_t>(min(64 * wave + lane, t.valid - 1)) * 4u
                                : static_cast<uint32_t>(lane) * 4u;
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                  :
                  : "v"(voff), "s"(base), "s"(ids_l)
                  : "memory", "m0");

@@ -28,9 +28,12 @@ constexpr int kPipeThreads = 256;    // 4 waves
 // LDS byte address lds_base + 16 l.  Issued through inline asm so that the
 // compiler does not see an LDS write it cannot place relative to the reads of
 // the other stages (it would drain every load before each read); the waits
-// are explicit instead.  The instruction has no register results.
+// are explicit instead.  The instruction has no register results.  Between a
+// scalar write of m0 and a load that takes its LDS address from it the hardware
+// needs one wait state, which the compiler does not add inside inline asm: the
+// s_nop here and in the other direct loads.
 __device__ __forceinline__ void dma16(const void* gptr, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                :
                : "v"(gptr), "s"(lds_base)
                : "memory", "m0");

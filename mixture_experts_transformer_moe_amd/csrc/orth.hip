@@ -107,7 +107,7 @@ __device__ __forceinline__ int run_off(int r, int h, int o) {
 }
 
 __device__ __forceinline__ void dma_run(const void* base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                :
                : "v"(voff), "s"(base), "s"(lds)
                : "memory", "m0");
