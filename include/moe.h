@@ -453,7 +453,8 @@ int moe_norm_forward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, co
                      void* y, float* mean, float* rstd, void* stream);
 
 /* Bytes of workspace moe_norm_backward needs for its column sums (0 for sizes
- * it rejects, and for rows == 0). */
+ * it rejects, and for rows == 0).  Does not shrink as rows grow: the workspace of
+ * the largest batch serves the smaller ones of the same width. */
 size_t moe_norm_workspace_bytes(int64_t rows, int32_t cols);
 
 /* Backward of moe_norm_forward: with h = (x - mean) rstd, t = dy gamma, per row

@@ -517,12 +517,10 @@ NormForm form_of(int64_t rows, int cols, int n) {
   return {0, 0};
 }
 
-// Workgroups: what the CUs hold at once by the kernels' registers, and the
-// same number of rows for each (2048 workgroups instead of 1536 for 32768 x
-// 2048, a second round for some: 124 us instead of 99).  A backward pass of few
-// rounds takes one a CU, for fewer partial sums (2048 x 2048 in bf16: 13.3 us
-// instead of 15.2 with two).
-int grid_of(int64_t rows, NormForm f, bool backward) {
+// Workgroups: at most what the CUs hold at once by the kernels' registers.  A
+// backward pass of few rounds takes one a CU, for fewer partial sums (2048 x 2048
+// in bf16: 13.3 us instead of 15.2 with two).  Grows with the rows.
+int64_t most_of(int64_t rows, NormForm f, bool backward) {
   const int64_t need = (rows + groups_of(f.tpr, backward) - 1) / groups_of(f.tpr, backward);
   int per_cu = f.tpr == 1024 ? 1 : f.ch == 1 ? 6 : f.ch == 2 ? 4 : 3;
   if (backward) {
@@ -532,7 +530,14 @@ int grid_of(int64_t rows, NormForm f, bool backward) {
     if (need <= 4 * 256) per_cu = 1;
   }
   const int64_t most = 256 * per_cu;
-  if (need <= most) return static_cast<int>(need);
+  return need < most ? need : most;
+}
+
+// The same number of rows for each workgroup (2048 workgroups instead of 1536 for
+// 32768 x 2048, forward, a second round for some: 124 us instead of 99).
+int grid_of(int64_t rows, NormForm f, bool backward) {
+  const int64_t need = (rows + groups_of(f.tpr, backward) - 1) / groups_of(f.tpr, backward);
+  const int64_t most = most_of(rows, f, backward);
   const int64_t each = (need + most - 1) / most;
   return static_cast<int>((need + each - 1) / each);
 }
@@ -567,14 +572,15 @@ void with_form(NormForm f, F&& go) {
 }  // namespace
 
 size_t norm_workspace_bytes(int64_t rows, int cols) {
-  // the most workgroups of any form, two sums each
-  size_t most = 0;
-  for (int n = 4; n <= 8; n += 4) {
-    const NormForm f = form_of(rows, cols, n);
-    const size_t b = static_cast<size_t>(grid_of(rows, f, true)) * 2 * cols * sizeof(float);
-    most = b > most ? b : most;
-  }
-  return (most + 255) & ~static_cast<size_t>(255);
+  // the most workgroups of any form of this many rows or fewer, two sums each: a
+  // batch's workspace also serves smaller ones
+  int64_t most = 0;
+  for (int n = 4; n <= 8; n += 4)
+    for (int64_t r : {rows < kManyRows ? rows : int64_t{kManyRows - 1}, rows}) {
+      const int64_t groups = most_of(r, form_of(r, cols, n), true);
+      most = groups > most ? groups : most;
+    }
+  return (static_cast<size_t>(most) * 2 * cols * sizeof(float) + 255) & ~static_cast<size_t>(255);
 }
 
 hipError_t launch_norm_forward(bool layer, int64_t rows, int cols, bool bf16, const void* x, const void* residual,
