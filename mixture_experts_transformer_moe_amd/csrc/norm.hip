@@ -550,10 +550,15 @@ void launch_fwd(const NormArgs& a, int grid, hipStream_t st) {
 template <typename T, int CH, int TPR>
 void launch_bwd(const NormArgs& a, int sums, hipStream_t st) {
   constexpr int kThreads = threads_of(TPR, true);
-  if (sums == kOwnSums)
-    norm_backward_kernel<T, CH, TPR, kOwnSums><<<a.row_blocks + (a.cols + kThreads / 32 - 1) / (kThreads / 32),
-                                                 kThreads, 0, st>>>(a);
-  else if (sums == kSumBoth) norm_backward_kernel<T, CH, TPR, kSumBoth><<<a.row_blocks, kThreads, 0, st>>>(a);
+  // (few rows: one of the forms that form_of gives them)
+  if constexpr (CH == 1 || TPR == 1024) {
+    if (sums == kOwnSums) {
+      norm_backward_kernel<T, CH, TPR, kOwnSums><<<a.row_blocks + (a.cols + kThreads / 32 - 1) / (kThreads / 32),
+                                                   kThreads, 0, st>>>(a);
+      return;
+    }
+  }
+  if (sums == kSumBoth) norm_backward_kernel<T, CH, TPR, kSumBoth><<<a.row_blocks, kThreads, 0, st>>>(a);
   else norm_backward_kernel<T, CH, TPR, kSumGamma><<<a.row_blocks, kThreads, 0, st>>>(a);
 }
 
