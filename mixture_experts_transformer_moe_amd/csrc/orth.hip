@@ -269,6 +269,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
   constexpr bool kSym = MODE <= kMul;
   constexpr bool kTr = !kSym;
   constexpr bool kOut = MODE >= kFinal;
+  static_assert(WB == 2 || WB == 4, "a wave owns 2 x 2 or 4 x 4 blocks");
   constexpr int TB = 2 * WB;
   constexpr int kOpBytes = TB * 2048;               // one operand of a stage
   constexpr int kStage = 2 * kOpBytes;
@@ -297,8 +298,8 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     int mat, rb, cb;                                // first row block and column block
   };
   // Sources of this wave's loads: kPtr pointers of 2 KB pieces for each
-  // operand (WB == 1: 1 KB), advanced stage by stage through the tile.
-  constexpr int kPtr = WB > 1 ? WB / 2 : 1;
+  // operand, advanced stage by stage through the tile.
+  constexpr int kPtr = WB / 2;
   const unsigned char* src[2 * kPtr];
   auto locate = [&](int ti) __attribute__((always_inline)) {
     Tile t;
@@ -326,13 +327,13 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
     const unsigned char* q = reinterpret_cast<const unsigned char*>(jb.q + t.mat * g.q_stride);
 #pragma unroll
     for (int k = 0; k < kPtr; ++k) {
-      // kilobyte of the operand's stage; blocks past the matrix repeat its
-      // last one (in bounds, never stored)
-      const int lin = WB > 1 ? wave * WB + 2 * k : wave;
-      const int rb = min(t.rb + (lin >> 1), g.mb - 1), cb = min(t.cb + (lin >> 1), g.nb - 1);
-      src[k] = uniform(p + (static_cast<size_t>(rb) * (g.K >> 4) + (lin & 1)) * 1024);
-      src[kPtr + k] = uniform(q + (kTr ? static_cast<size_t>(2 * cb + (lin & 1)) * 1024
-                                       : (static_cast<size_t>(cb) * (g.K >> 4) + (lin & 1)) * 1024));
+      // block of the operand's stage; blocks past the matrix repeat its last one
+      // (in bounds, never stored)
+      const int b = wave * kPtr + k;
+      const int rb = min(t.rb + b, g.mb - 1), cb = min(t.cb + b, g.nb - 1);
+      src[k] = uniform(p + static_cast<size_t>(rb) * (g.K >> 4) * 1024);
+      src[kPtr + k] = uniform(q + (kTr ? static_cast<size_t>(2 * cb) * 1024
+                                       : static_cast<size_t>(cb) * (g.K >> 4) * 1024));
     }
   };
   const uint32_t q_step = kTr ? static_cast<uint32_t>(g.nb) * 2048u : 2048u;   // bytes a stage advances q
@@ -413,11 +414,8 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
           op(WB * i + j);
           __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-      for (int k = WB * WB; k < 2 * WB; ++k) op(k);
     };
-    constexpr int kOps = WB * WB > 2 * WB ? WB * WB : 2 * WB;
-    constexpr int kEvery = kOps / (2 * WB);         // one operand read (and load) per so many MFMAs
+    constexpr int kEvery = WB / 2;                  // one operand read (and load) per so many MFMAs
 
     // The diagonal's part of x <- P x: in the stage that holds the rows of row
     // block i of the wave, its accumulators also take diag(e) times those rows
@@ -550,7 +548,7 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
       const int own = cur.rb + wr * WB;
       while (x < own) one(None{});
       one(std::integral_constant<int, 0>{});
-      if constexpr (WB > 1) one(std::integral_constant<int, 1>{});
+      one(std::integral_constant<int, 1>{});
       if constexpr (WB > 2) one(std::integral_constant<int, 2>{});
       if constexpr (WB > 3) one(std::integral_constant<int, 3>{});
       while (x < nkb) one(None{});
