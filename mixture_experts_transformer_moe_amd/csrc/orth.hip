@@ -16,11 +16,11 @@
 // matter while Q(R) acts on them as a I, but does once the spectrum is flat.
 // Nor are three, nor those of a small matrix (m < 256), whose roundings average
 // over few terms.  Error against 64 bits, relative in norm, of rank-deficient
-// bf16 gradients (the output's own rounding to bf16 is 1.7e-3 of each):
+// gradients (the output's own rounding to bf16 is 1.7e-3 of each):
 //                                         1+1+1+1+1  2+1+1+1  3+1+1   3+2
-//   1024 x 2048, rank 128                 1.8e-3     1.8e-3   1.9e-3  2.8e-3
-//   256 x 1024, rank 1 and noise of 1e-3  2.2e-3     2.4e-3   6.3e-3  6.4e-3
-//   32 x 32, rank 16                      2.6e-3     3.4e-3   7.4e-3
+//   1024 x 2048, rank 128                 1.9e-3     1.9e-3   2.0e-3  2.3e-3
+//   256 x 1024, rank 1 and noise of 1e-3  1.9e-3     2.0e-3   3.2e-3  3.1e-3
+//   32 x 32, rank 16                      2.2e-3     2.4e-3   5.3e-3  5.6e-3
 //
 // Numbers.  Products run on fp16 operands with fp32 accumulation: singular
 // directions far below the largest are amplified by a^5 = 485, and bf16's 8
@@ -33,9 +33,11 @@
 //     otherwise be the largest error;
 //   * x is stored as fp16 hi + lo (22 bits).  M x and diag(d) x read hi (the
 //     latter as MFMAs with a diagonal operand, in the stage that holds the
-//     rows), the epilogue adds d_i lo_ij.  The x before the last step has no
-//     low part: what its rounding adds is amplified by a at most (first line of
-//     the table above 1.8e-3 -> 1.9e-3; without it in the last two 2.8e-3).
+//     rows), the epilogue adds g_i lo_ij, g_i near a or d_i (LowGain below; with
+//     d_i throughout 32 x 32 of rank 16 is 3.8e-3 off, after 8 steps 3e-2).  The x
+//     before the last step has no low part: what its rounding adds is amplified
+//     by a at most (second line of the table above 1.7e-3 -> 2.0e-3; without it
+//     in the last two 2.9e-3).
 // Powers of two keep fp16 away from its subnormals: x and R are stored times
 // 2^12 (|x|, |R| < 2), Q and Q2 Q1 times 2^8 (|Q2 Q1| <= a^2 = 12).
 //
@@ -75,6 +77,31 @@ constexpr int kMinPad = 128;          // smallest padded side: a tile has at lea
 // kFinal: x <- P x into the caller's matrix, x without a low part (kFinalLo: with)
 enum { kGram = 0, kPoly = 1, kMul = 2, kApply = 3, kFinal = 4, kFinalLo = 5 };
 
+// What multiplies x's low part in x <- P x, P the polynomials of k steps.  The
+// product itself reads x's high part, so with g_i for the low part x is off by
+//   (P - a^k I) lo + (a^k - g_i) lo.
+// The first lies in the columns' span of x, since P - a^k I = b R + ..., and stays
+// as small as it is.  The second does not: each step to follow multiplies by a
+// what lies outside the span.  So g_i = a^k while steps follow.  With the last two
+// to follow, the first counts too, of an x whose rows are near unit vectors above
+// all; there P = a^k I - K, K a multiple of at most kappa of the projector on the
+// span, and K_ii / kappa tells how much of a row's unit vector the span holds:
+//   e_i = a^k - d_i = K_ii,  g_i = d_i + e_i (1 - e_i / kappa).
+// In the last two products nothing is amplified any more, and g_i = d_i.
+struct LowGain {
+  float a, w, k;            // a^k; 1, or 0 for g = d; 1 / kappa, or 0 for g = a^k
+  __device__ __forceinline__ float operator()(float d) const {
+    const float e = a - d;
+    return fmaf(fmaxf(fmaf(-e, k, w), 0.0f), e, d);
+  }
+};
+
+__host__ __device__ __forceinline__ LowGain low_gain(int taken, int after) {
+  constexpr float kKappa = kB * kB / (4.0f * kC);   // a - min Q
+  const float more = taken == 2 ? kA : 1.0f;
+  return {kA * more, after < 2 ? 0.0f : 1.0f, after == 2 ? 1.0f / (kKappa * more) : 0.0f};
+}
+
 struct OrthJob {
   const _Float16* p;        // row operand, [rows / 32][K / 16] blocks
   const _Float16* q;        // column operand; kApply, kFinal, kFinalLo: x hi, [K / 32][n / 16] blocks
@@ -85,6 +112,7 @@ struct OrthJob {
   _Float16* out_lo;         // kApply: the low part, or null
   float* dout;
   float sp, sq, so;         // stored scales of p, q and out
+  LowGain low;              // kApply: what x's low part is multiplied by
 };
 
 struct OrthArgs {
@@ -182,8 +210,9 @@ __device__ __forceinline__ void finish(float (&v)[8], const f16x8& a, const f16x
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= 1.0f / kSQ;
   } else {
+    const float d = MODE == kApply ? jb.low(dpi) : dpi;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fmaf(static_cast<float>(a[e]), dpi, v[e] * (1.0f / kSQ));
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(static_cast<float>(a[e]), d, v[e] * (1.0f / kSQ));
   }
 }
 
@@ -1460,9 +1489,13 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
           for (int st = 0; st < 2; ++st)
             y = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_run(xs + (kb * 2 * nb + 2 * j) * 1024, st, lane),
                                                        qa[2 * kb + st], y, 0, 0, 0);
-        const float di = qd[32 * i + r];
+        // (hi as the products read it, and what it leaves)
+        const float di = qd[32 * i + r], gain = low_gain(1, steps - 1 - step)(di);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) x[t][q] = fmaf(di, x[t][q], y[q] * (1.0f / kSQ));
+        for (int q = 0; q < 16; ++q) {
+          const float hi = static_cast<float>(static_cast<_Float16>(x[t][q]));
+          x[t][q] = fmaf(di, hi, fmaf(gain, x[t][q] - hi, y[q] * (1.0f / kSQ)));
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -1674,13 +1707,15 @@ hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, co
     launch_mode<kMul>(a, st);
   };
   bool has_lo = true;                           // x_0 has a low part
-  auto apply = [&](int q, int after) {          // x <- S[q] x, with `after` steps to follow
+  // x <- S[q] x, the polynomials of `taken` steps, with `after` steps to follow
+  auto apply = [&](int q, int taken, int after) {
     OrthArgs a = base;
     a.nb = p.np / 32;
     a.K = p.mp;
     a.p_stride = ss;
     a.q_stride = a.out_stride = xs;
-    a.job = {S[q], X[xi], X[xi + 1], D[q], nullptr, X[xi ^ 2], after > 1 ? X[(xi ^ 2) + 1] : nullptr, nullptr, kSQ, kSX, kSX};
+    a.job = {S[q], X[xi], X[xi + 1], D[q], nullptr, X[xi ^ 2], after > 1 ? X[(xi ^ 2) + 1] : nullptr, nullptr, kSQ, kSX, kSX,
+             low_gain(taken, after)};
     if (after > 0) launch_mode<kApply>(a, st);
     else if (has_lo) launch_mode<kFinalLo>(a, st);
     else launch_mode<kFinal>(a, st);
@@ -1697,12 +1732,12 @@ hipError_t launch_orthogonalize(int64_t count, int rows, int cols, bool bf16, co
     poly(V);                                    // Q2
     mul(product(V, kSQ, U, kSQ, T, kSQ));       // Q2 Q1
     left -= 2;
-    apply(T, left);
+    apply(T, 2, left);
   }
   while (left > 0) {
     gram();
     poly(U);
-    apply(U, --left);
+    apply(U, 1, --left);
   }
   return hipGetLastError();
 }
