@@ -67,24 +67,24 @@ GEMM_SOURCES = ("grouped_gemm.hip", "grouped_gemm_lds.hip", "grouped_gemm.h", "m
                 "moe_internal.h")
 TRAFFIC = {
     # workload: (FETCH_SIZE KiB, WRITE_SIZE KiB, sha256 of GEMM_SOURCES)
-    "prefill_outlier_bf16_t32768_d2048": (2220334.4, 296593.7,
-                                          "7a444bd95cd2e0f0d71c371dd3d20d23890a983b340c180b63e9797b254bd5ef"),
-    "xs2_bf16_t4096_d2048": (657312.4, 36864.3,
-                             "7a444bd95cd2e0f0d71c371dd3d20d23890a983b340c180b63e9797b254bd5ef"),
-    "m1_bf16_t8192_d4096": (3305043.9, 147597.8,
-                            "7a444bd95cd2e0f0d71c371dd3d20d23890a983b340c180b63e9797b254bd5ef"),
-    "m1_top16_bf16_t8192_d4096": (5444833.1, 278859.4,
-                                  "7a444bd95cd2e0f0d71c371dd3d20d23890a983b340c180b63e9797b254bd5ef"),
-    "decode_zipf_bf16_t32_d4096": (493915.0, 576.0,
-                                   "7a444bd95cd2e0f0d71c371dd3d20d23890a983b340c180b63e9797b254bd5ef"),
+    "prefill_outlier_bf16_t32768_d2048": (2185070.6, 296467.1,
+                                          "01483d277804a377da03ecbbe6987fa78da6eba32e816562cab95267a39570bf"),
+    "xs2_bf16_t4096_d2048": (660300.4, 36864.3,
+                             "01483d277804a377da03ecbbe6987fa78da6eba32e816562cab95267a39570bf"),
+    "m1_bf16_t8192_d4096": (3285855.4, 147585.4,
+                            "01483d277804a377da03ecbbe6987fa78da6eba32e816562cab95267a39570bf"),
+    "m1_top16_bf16_t8192_d4096": (5437448.4, 278867.0,
+                                  "01483d277804a377da03ecbbe6987fa78da6eba32e816562cab95267a39570bf"),
+    "decode_zipf_bf16_t32_d4096": (493915.4, 576.0,
+                                   "01483d277804a377da03ecbbe6987fa78da6eba32e816562cab95267a39570bf"),
 }
 
 
 # The same for one launch of the weight-gradient kernel in the training pass.
 WGRAD_SOURCES = ("wgrad.hip", "lds_dma.h", "moe_internal.h")
 WGRAD_TRAFFIC = {
-    "xs2_train_bf16_t4096_d2048": (250806.5, 1581073.2,
-                                   "ec40073f6eb5ff1c325864b70a7ecb9ecbf6943d6d6224261cb66c932b35412f"),
+    "xs2_train_bf16_t4096_d2048": (250870.2, 1581072.2,
+                                   "54d12fec9e89ab8f82ff4455423520917b10b8bb89ba4a0e5ba57a768c5b7098"),
 }
 
 
