@@ -1123,16 +1123,17 @@ __global__ __launch_bounds__(256) void orth_pack_kernel(const T* g, const float*
 // ------------------------------------------------------------ small matrices
 // A whole update in one workgroup, for matrices whose x fits its LDS: the
 // launches of the general path would be most of the time (1 matrix of 128 x 128:
-// 32 us against 58, of 128 x 400: 58 against 61; 256 of 128 x 128: 34 against
-// 120, of 64 x 1000: 60 against 349).
+// 30 us against 58, of 128 x 400: 55 against 61; 256 of 128 x 128: 32 against
+// 120, of 64 x 1000: 58 against 349).
 //   * x stays in registers, in fp32 and in accumulator order: wave w owns the
 //     blocks w, w + 8, ... (row block t mod MB, column block t / MB); its fp16
 //     copy, the products' operand, is in LDS in blocks as above;
-//   * the symmetric matrix, R and then in its place Q, is in LDS with zeros on
-//     the diagonal and the diagonal in fp32 beside it;
+//   * the symmetric matrix, R and then in its place Q, is in LDS with zeros (Q:
+//     what LowGain takes off the diagonal) on the diagonal and the diagonal in
+//     fp32 beside it;
 //   * a step: R's lower blocks dealt to the waves (for few blocks also K, the
 //     parts joined through LDS in order), Q's likewise, then every wave its
-//     blocks of Q x; the block's elementwise part d_i x_ij is in fp32.
+//     blocks of Q x; the block's elementwise part g_i x_ij is in fp32.
 constexpr int kResMaxMB = 6;
 constexpr int kResBlocks = 8;                         // blocks of x a wave owns at most
 constexpr int kResLoads = 4;                          // blocks whose input is loaded at once
@@ -1415,6 +1416,7 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
     }
     __syncthreads();
     // ---- Q = a I + b R + c R^2, kept in registers until R has been read
+    const LowGain low = low_gain(1, steps - 1 - step);
     f16x8 qw[kQMine][2];
 #pragma unroll
     for (int k = 0; k < kQMine; ++k) {
@@ -1444,12 +1446,15 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
           }
           const int at = r - 16 * p - 8 * h;
           if (i == j && at >= 0 && at < 8) {
+            // d hi + g lo as (d - g) hi, by the product, + g x (g as rounding d - g leaves it)
+            float d = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e == at) {
-                qd[32 * i + r] = fmaf(v[e], 1.0f / kSQ, fmaf(di, fmaf(kC, di, kB), kA));
-                v[e] = 0.0f;
-              }
+            for (int e = 0; e < 8; ++e) d = e == at ? v[e] : d;
+            d = fmaf(d, 1.0f / kSQ, fmaf(di, fmaf(kC, di, kB), kA));
+            const float s = static_cast<float>(static_cast<_Float16>((d - low(d)) * kSQ));
+            qd[32 * i + r] = fmaf(s, -1.0f / kSQ, d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e == at ? s : v[e];
           }
           qw[k][p] = to_f16(v);
         }
@@ -1489,13 +1494,9 @@ __global__ __launch_bounds__(kSThreads) void orth_resident_kernel(const T* gp, f
           for (int st = 0; st < 2; ++st)
             y = __builtin_amdgcn_mfma_f32_32x32x16_f16(tr_run(xs + (kb * 2 * nb + 2 * j) * 1024, st, lane),
                                                        qa[2 * kb + st], y, 0, 0, 0);
-        // (hi as the products read it, and what it leaves)
-        const float di = qd[32 * i + r], gain = low_gain(1, steps - 1 - step)(di);
+        const float di = qd[32 * i + r];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float hi = static_cast<float>(static_cast<_Float16>(x[t][q]));
-          x[t][q] = fmaf(di, hi, fmaf(gain, x[t][q] - hi, y[q] * (1.0f / kSQ)));
-        }
+        for (int q = 0; q < 16; ++q) x[t][q] = fmaf(di, x[t][q], y[q] * (1.0f / kSQ));
       }
       __builtin_amdgcn_sched_barrier(0);
     }
