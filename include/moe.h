@@ -447,7 +447,8 @@ typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
  *                NULL; mean is not written for MOE_NORM_RMS
  * sum or y may be x or residual itself (not each other); no other overlap.
  * cols <= 16384 (else MOE_ERR_UNSUPPORTED), any width from 1; rows >= 0.  The
- * statistics are fp32, the variance summed around the mean. */
+ * statistics are fp32, the variance summed around the mean: a row whose sum of
+ * squares leaves fp32 (elements near 1e19) has rstd 0. */
 int moe_norm_forward(int32_t kind, int64_t rows, int32_t cols, int32_t dtype, const void* x,
                      const void* residual, const float* gamma, const float* beta, float eps, void* sum,
                      void* y, float* mean, float* rstd, void* stream);

@@ -10,10 +10,15 @@
 //   ds = rstd (t - h sum(t h) / D - sum t / D [layer norm only]) + dsum
 //   dgamma = sum over rows of dy h,  dbeta = sum over rows of dy
 //
-// Both are bound by HBM: each input is read once and each output written once.
+// Both are bound by HBM: each input is read once and each output written once
+// (of few rows, the backward pass reads x and dy a second time, for the columns).
 //   * A row lives in the registers of a group of 16 to 1024 threads, CH 16-byte
 //     vectors a thread, so the variance is summed around the mean (no
-//     cancellation) without a second read.
+//     cancellation) without a second read.  Past 8192 columns the backward pass
+//     with column sums needs more than the 128 registers a thread of 1024 has,
+//     and spills: 36 bytes a thread in bf16 (dbeta too: 108), 108 in fp32 (184).
+//     4096 x 16384 with dsum, bf16: 102 us without sums (5.3 TB/s), 113 with
+//     dgamma's (4.7), 148 with both (3.6); fp32: 211, 222 and 261 (4.1).
 //   * Groups walk the rows with the grid as stride; gamma and beta stay in
 //     registers, and in the backward pass so do the column sums of dgamma and
 //     dbeta.  Each workgroup writes its sums once, to the workspace, and a

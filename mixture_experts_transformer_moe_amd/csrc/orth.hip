@@ -550,12 +550,11 @@ __global__ __launch_bounds__(kOThreads, WB == 4 ? 1 : 2) void orth_gemm_kernel(O
 #pragma unroll 1
         for (int x = 0; x < kStages; ++x) stage(tag);
       };
-      // In a tile of R on the diagonal the blocks above it are left out (the
-      // chip runs at its power limit here, so MFMAs saved are time saved: 32
-      // matrices of 2048 x 4096 542 -> 518 us): the upper right wave only
-      // loads, the two waves on the diagonal compute their lower blocks.  The
-      // other modes' epilogue loads would cross the branches, which waits for
-      // them (the same matrices, Q: 314 -> 377 us).
+      // In a tile of R on the diagonal the blocks above it are left out (32
+      // matrices of 2048 x 4096 542 -> 518 us): the upper right wave only loads,
+      // the two waves on the diagonal compute their lower blocks.  The other
+      // modes' epilogue loads would cross the branches, which waits for them
+      // (the same matrices, Q: 314 -> 377 us).
       if (MODE != kGram || cur.rb != cur.cb || wr > wc) {
         loop(None{});
       } else if (wr == wc) {
