@@ -82,12 +82,17 @@ enum { kGram = 0, kPoly = 1, kMul = 2, kApply = 3, kFinal = 4, kFinalLo = 5 };
 //   (P - a^k I) lo + (a^k - g_i) lo.
 // The first lies in the columns' span of x, since P - a^k I = b R + ..., and stays
 // as small as it is.  The second does not: each step to follow multiplies by a
-// what lies outside the span.  So g_i = a^k while steps follow.  With the last two
-// to follow, the first counts too, of an x whose rows are near unit vectors above
-// all; there P = a^k I - K, K a multiple of at most kappa of the projector on the
-// span, and K_ii / kappa tells how much of a row's unit vector the span holds:
+// what lies outside the span.  So g_i = a^k while steps follow.  With two to
+// follow the first part counts as well, most of all for a matrix near a diagonal
+// one, which d_i would have exact.  By then P = a^k I - K, K near kappa times the
+// projector on the span, so K_ii / kappa tells how much of row i's unit vector the
+// span holds:
 //   e_i = a^k - d_i = K_ii,  g_i = d_i + e_i (1 - e_i / kappa).
-// In the last two products nothing is amplified any more, and g_i = d_i.
+// In the last two products nothing is amplified any more, and g_i = d_i.  (Off by,
+// with d_i throughout / a^k also with two to follow / as here: 32 x 32 of rank 16
+// 3.8e-3 / 2.1e-3 / 2.2e-3, 333 x 1001 of rank 100 2.5e-3 / 2.0e-3 / 2.0e-3, the
+// largest element's error of a diagonal matrix over three decades, in half steps of
+// bf16, 1.56 / 1.91 / 1.56.)
 struct LowGain {
   float a, w, k;            // a^k; 1, or 0 for g = d; 1 / kappa, or 0 for g = a^k
   __device__ __forceinline__ float operator()(float d) const {

@@ -46,7 +46,7 @@ def check(out, want, where, bound=2.6e-3):
     assert np.linalg.norm(to_f64(out) - want) <= bound * n, where
 
 
-@pytest.mark.parametrize("steps", [1, 2, 3, 6])
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6])
 @pytest.mark.parametrize("tall", [False, True], ids=["wide", "tall"])
 @pytest.mark.parametrize("path", list(PATHS))
 def test_steps(path, tall, steps):
