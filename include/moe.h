@@ -510,9 +510,11 @@ size_t moe_orthogonalize_workspace_bytes(int64_t count, int32_t rows, int32_t co
  * error against 64 bits, relative in norm, of which 1.66e-3 is the rounding of
  * the bf16 output: 1.7e-3 to 2.1e-3 at 5 steps for gradients with 100 rows and
  * columns or more, up to 2.8e-3 for smaller ones of low rank or repeated rows
- * (5e-3 below 8 rows); up to 4e-3 at 8 steps, 5e-3 at 16.  Bit-reproducible for
- * the same sizes and count; a matrix's bits may depend on how many are given
- * with it.
+ * (5e-3 below 8 rows); up to 4e-3 at 8 steps (5e-3 for equal elements), 5e-3 at 16
+ * where u has full rank.  Past 8 steps what a matrix of exactly lower rank has
+ * outside its span, about the rounding of fp32, grows to the size of the result,
+ * as it does in fp32 products.  Bit-reproducible for the same sizes and count; a
+ * matrix's bits may depend on how many are given with it.
  * The workspace holds nothing between calls; calls and captured graphs that may
  * run at the same time need one each.
  * rows, cols <= 65536, rows * cols < 2^30, count <= 65535, count * rows * cols <

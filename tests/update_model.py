@@ -35,7 +35,7 @@ class Case:
 
     @property
     def name(self):
-        return f"{self.count}x{self.rows}x{self.cols} rank {self.rank} steps {self.steps}" + (" noise" if self.noise else "")
+        return f"{self.count}x{self.rows}x{self.cols} rank {self.rank} steps {self.steps}" + (" noise" if self.noise else "") + f" {self.dtype}"
 
 
 CASES = [
@@ -61,6 +61,11 @@ CASES = [
     Case(2, 333, 1001, 100, 2.3e-3, steps=8),
     Case(2, 333, 1001, 100, 3.6e-3, steps=16),
     Case(2, 1001, 333, 100, 2.4e-3, steps=6),
+    # exactly of low rank, but for the rounding to fp32: any step that left the span would show
+    Case(64, 16, 200, 8, 3.0e-3, steps=7, dtype="f32"),
+    Case(64, 32, 32, 16, 3.4e-3, steps=8, dtype="f32"),
+    Case(2, 333, 1001, 100, 2.7e-3, steps=8, dtype="f32"),
+    Case(2, 2048, 256, 64, 2.6e-3, steps=8, dtype="f32"),
 ]
 
 
