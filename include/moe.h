@@ -300,6 +300,71 @@ int moe_grouped_down_fp8(const moe_shape* shape, const void* h, const int32_t* o
                          const void* w_down, const float* w_down_scale, const void* ws_down,
                          const float* ws_down_scale, void* y_perm, void* y_shared, void* stream);
 
+/* ---- 4-bit expert weights ------------------------------------------------
+ * The pages list INT4 recipes for the MoE layers beside FP8's ("Laguna M.1/XS.2
+ * Technical Report", Key claims) without encoding details; this library's reading
+ * (symmetric, one scale a row and group of consecutive columns):
+ *   - code[r,c] an integer -8..7; scale[r,g] bf16, g = c / group, group 32, 64 or 128;
+ *   - the layer runs with the weights code * scale.  The products take the codes
+ *     as they are (exact) with the bf16 activations, fp32 accumulation, and
+ *     apply the scale to each group's fp32 sum;
+ *   - moe_quantize_weights_int4: scale = max |w| of the group / 7 in fp32, rounded
+ *     to bf16 (1 where that gives zero); code = w / scale (fp32 quotient) to the
+ *     nearest integer, ties to even, clamped to -8..7.
+ * Activations stay bf16 (shape dtype MOE_BF16; anything else returns
+ * MOE_ERR_UNSUPPORTED).  Weights must be finite (non-finite inputs give
+ * unspecified codes); scales may be any bf16 value. */
+
+/* Bytes of `count` 4-bit [rows, cols] matrices (count * rows * cols / 2); 0 unless
+ * rows is a multiple of 16 and cols of 128. */
+size_t moe_int4_packed_bytes(int64_t count, int32_t rows, int32_t cols);
+
+/* Quantise bf16 weights to 4 bits and pack them for moe_grouped_gate_up_int4 /
+ * moe_grouped_down_int4 (a one-time pass when weights are loaded).
+ *   w       [count, rows, cols] bf16, row-major, rows = output rows (e.g.
+ *           w_gate_up as [E, 2F, D], w_down as [E, D, F])
+ *   w_int4  moe_int4_packed_bytes(count, rows, cols) bytes, out
+ *   scales  [count, rows, cols / group] bf16, out
+ *   rows % 16 == 0, cols % 128 == 0 (else MOE_ERR_INVALID_ARG); the three buffers
+ *   must not overlap.
+ * Layout: matrix i starts at byte i * rows * cols / 2; in it, the code of (r, c),
+ * stored as code + 8, sits in the 4 bits at 4 ((c % 8) / 2 + 4 (c % 2)) of the
+ * little-endian 32-bit word at byte
+ *   ((r / 16) * (cols / 128) + c / 128) * 1024 + ((r % 16) + 16 * ((c % 32) / 8)) * 16
+ *     + ((c % 128) / 32) * 4,
+ * i.e. 16 x 128 blocks of 1 KB in which lane l's 16 bytes are its codes of four
+ * 32-wide K steps of a 16x16x32 MFMA operand. */
+int moe_quantize_weights_int4(const void* w, void* w_int4, void* scales, int64_t count, int32_t rows,
+                              int32_t cols, int32_t group, void* stream);
+
+/* Pack codes that are already quantised (a 4-bit checkpoint's) into that layout.
+ *   codes   [count, rows, cols / 2] bytes, row-major: byte j of a row holds
+ *           code + 8 of column 2j in its low half and of column 2j + 1 in its high
+ *           half
+ *   w_int4  moe_int4_packed_bytes(count, rows, cols) bytes, out; must not overlap
+ *           codes
+ * The scales go to the products as they are, row-major [count, rows, cols / group]. */
+int moe_pack_weights_int4(const void* codes, void* w_int4, int64_t count, int32_t rows, int32_t cols,
+                          void* stream);
+
+/* moe_grouped_gate_up with 4-bit weights: the same computation and buffers, with
+ * w_gate_up / ws_gate_up replaced by packed codes and their scales, one group
+ * size for all (w_gate_up_scale [E, 2F, D / group] bf16, ws_gate_up_scale
+ * [2Fs, D / group]; the shared pair is ignored, may be NULL, when Fs == 0).
+ * Any batch: one token to long prefills.  Rows of h past offsets[E] (slots that
+ * are not routed) are left as they were.  h must not overlap an input. */
+int moe_grouped_gate_up_int4(const moe_shape* shape, int32_t group, const void* x_perm,
+                             const int32_t* sorted_token, const void* x, const int32_t* offsets,
+                             const void* w_gate_up, const void* w_gate_up_scale, const void* ws_gate_up,
+                             const void* ws_gate_up_scale, void* h, void* stream);
+
+/* moe_grouped_down with 4-bit weights (w_down_scale [E, D, F / group] bf16,
+ * ws_down_scale [D, Fs / group]).  y_perm and y_shared must not overlap an input
+ * or each other. */
+int moe_grouped_down_int4(const moe_shape* shape, int32_t group, const void* h, const int32_t* offsets,
+                          const void* w_down, const void* w_down_scale, const void* ws_down,
+                          const void* ws_down_scale, void* y_perm, void* y_shared, void* stream);
+
 /* Combine: out[t] = y_shared[t] + sum_{j=0..k-1} (alpha * topk_w[t,j]) * y_perm[slot_of[t,j]],
  * accumulated in fp32 in slot order and rounded once to elem ("Laguna M.1/XS.2
  * Technical Report", Key claims: routed output modulated by alpha before

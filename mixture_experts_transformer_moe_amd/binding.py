@@ -34,7 +34,9 @@ EXPORTS = ("moe_version", "moe_status_string", "moe_last_error", "moe_workspace_
            "moe_combine_backward", "moe_grouped_backward_h", "moe_grouped_backward_x",
            "moe_weight_grads", "moe_bias_grad", "moe_shared_ffn", "moe_permute_static",
            "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward",
-           "moe_orthogonalize_workspace_bytes", "moe_orthogonalize")
+           "moe_orthogonalize_workspace_bytes", "moe_orthogonalize",
+           "moe_int4_packed_bytes", "moe_quantize_weights_int4", "moe_pack_weights_int4",
+           "moe_grouped_gate_up_int4", "moe_grouped_down_int4")
 
 
 class moe_shape(ctypes.Structure):
@@ -138,6 +140,17 @@ def lib() -> ctypes.CDLL:
         L.moe_orthogonalize_workspace_bytes.argtypes = [i64, i32, i32]
         L.moe_orthogonalize.restype = ctypes.c_int
         L.moe_orthogonalize.argtypes = [i64, i32, i32, i32, _P, _P, f32, i32, i32, f32, f32, _P, _P, size, _P]
+        # 4-bit expert weights
+        L.moe_int4_packed_bytes.restype = size
+        L.moe_int4_packed_bytes.argtypes = [i64, i32, i32]
+        L.moe_quantize_weights_int4.restype = ctypes.c_int
+        L.moe_quantize_weights_int4.argtypes = [_P, _P, _P, i64, i32, i32, i32, _P]
+        L.moe_pack_weights_int4.restype = ctypes.c_int
+        L.moe_pack_weights_int4.argtypes = [_P, _P, i64, i32, i32, _P]
+        L.moe_grouped_gate_up_int4.restype = ctypes.c_int
+        L.moe_grouped_gate_up_int4.argtypes = [_SP, i32] + [_P] * 10
+        L.moe_grouped_down_int4.restype = ctypes.c_int
+        L.moe_grouped_down_int4.argtypes = [_SP, i32] + [_P] * 9
         _lib = L
     return _lib
 
@@ -293,6 +306,82 @@ def moe_grouped_down_fp8(shape, h, offsets, w_down, w_down_scale, ws_down, ws_do
            "moe_grouped_down_fp8")
 
 
+def moe_int4_packed_bytes(count, rows, cols) -> int:
+    return int(lib().moe_int4_packed_bytes(int(count), int(rows), int(cols)))
+
+
+def moe_quantize_weights_int4(w, w_int4, scales, count, rows, cols, group, stream=None):
+    dev, n = w.get_device(), int(count) * int(rows) * int(cols)
+    _check(lib().moe_quantize_weights_int4(
+        _flat(w, n, torch.bfloat16, dev, "w"), _flat(w_int4, n // 2, torch.uint8, dev, "w_int4"),
+        _flat(scales, n // group if group else 0, torch.bfloat16, dev, "scales"), int(count), int(rows), int(cols),
+        int(group), _stream_on(stream, dev)), "moe_quantize_weights_int4")
+
+
+def moe_pack_weights_int4(codes, w_int4, count, rows, cols, stream=None):
+    dev, n = codes.get_device(), int(count) * int(rows) * int(cols) // 2
+    _check(lib().moe_pack_weights_int4(_flat(codes, n, torch.uint8, dev, "codes"),
+                                       _flat(w_int4, n, torch.uint8, dev, "w_int4"), int(count), int(rows), int(cols),
+                                       _stream_on(stream, dev)), "moe_pack_weights_int4")
+
+
+def _int4_buffer(count, rows, cols, device) -> torch.Tensor:
+    nbytes = moe_int4_packed_bytes(count, rows, cols)
+    if nbytes == 0 and count * rows * cols > 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, f"moe_int4_packed_bytes: cannot pack [{count}, {rows}, {cols}]")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def quantize_int4(w: torch.Tensor, group: int = 128, stream=None):
+    """4-bit codes (flat uint8, packed) and scales (bfloat16 [count, rows, cols / group])
+    of a bf16 [rows, cols] or [count, rows, cols] weight tensor."""
+    count, rows, cols = (1, *w.shape) if w.dim() == 2 else w.shape
+    codes = _int4_buffer(count, rows, cols, w.device)
+    if group not in (32, 64, 128):
+        raise MoEError(MOE_ERR_INVALID_ARG, f"group = {group} is not 32, 64 or 128")
+    scales = torch.empty((count, rows, cols // group), dtype=torch.bfloat16, device=w.device)
+    moe_quantize_weights_int4(w.contiguous(), codes, scales, count, rows, cols, group, stream)
+    return codes, scales
+
+
+def pack_int4(codes: torch.Tensor, stream=None) -> torch.Tensor:
+    """Packed copy (flat uint8) of row-major 4-bit codes [rows, cols / 2] or
+    [count, rows, cols / 2], two a byte as include/moe.h has them."""
+    count, rows, half = (1, *codes.shape) if codes.dim() == 2 else codes.shape
+    out = _int4_buffer(count, rows, 2 * half, codes.device)
+    moe_pack_weights_int4(codes.contiguous(), out, count, rows, 2 * half, stream)
+    return out
+
+
+def moe_grouped_gate_up_int4(shape, group, x_perm, sorted_token, x, offsets, w_gate_up, w_gate_up_scale,
+                             ws_gate_up, ws_gate_up_scale, h, stream=None):
+    dev, u8, bf, i32 = x.get_device(), torch.uint8, torch.bfloat16, torch.int32
+    T, D, E, F, Fs, S = shape.T, shape.D, shape.E, shape.F, shape.Fs, shape.T * shape.k
+    n, ns, g = E * 2 * F * D, 2 * Fs * D, group or 1
+    _check(lib().moe_grouped_gate_up_int4(
+        ctypes.byref(shape), group, _flat(x_perm, S * D, bf, dev, "x_perm"),
+        _flat(sorted_token, S, i32, dev, "sorted_token") if x_perm is None else None, _flat(x, T * D, bf, dev, "x"),
+        _flat(offsets, E + 1, i32, dev, "offsets"), _flat(w_gate_up, n // 2, u8, dev, "w_gate_up"),
+        _flat(w_gate_up_scale, n // g, bf, dev, "w_gate_up_scale"),
+        _flat(ws_gate_up, ns // 2, u8, dev, "ws_gate_up") if Fs else None,
+        _flat(ws_gate_up_scale, ns // g, bf, dev, "ws_gate_up_scale") if Fs else None,
+        _flat(h, S * F + T * Fs, bf, dev, "h"), _stream_on(stream, dev)), "moe_grouped_gate_up_int4")
+
+
+def moe_grouped_down_int4(shape, group, h, offsets, w_down, w_down_scale, ws_down, ws_down_scale, y_perm,
+                          y_shared, stream=None):
+    dev, u8, bf = h.get_device(), torch.uint8, torch.bfloat16
+    T, D, E, F, Fs, S = shape.T, shape.D, shape.E, shape.F, shape.Fs, shape.T * shape.k
+    n, ns, g = E * D * F, D * Fs, group or 1
+    _check(lib().moe_grouped_down_int4(
+        ctypes.byref(shape), group, _flat(h, S * F + T * Fs, bf, dev, "h"),
+        _flat(offsets, E + 1, torch.int32, dev, "offsets"), _flat(w_down, n // 2, u8, dev, "w_down"),
+        _flat(w_down_scale, n // g, bf, dev, "w_down_scale"), _flat(ws_down, ns // 2, u8, dev, "ws_down") if Fs else None,
+        _flat(ws_down_scale, ns // g, bf, dev, "ws_down_scale") if Fs else None,
+        _flat(y_perm, S * D, bf, dev, "y_perm"), _flat(y_shared, T * D, bf, dev, "y_shared") if Fs else None,
+        _stream_on(stream, dev)), "moe_grouped_down_int4")
+
+
 def moe_combine(shape, y_perm, y_shared, slot_of, topk_w, out, stream=None):
     _check(lib().moe_combine(ctypes.byref(shape), _ptr(y_perm), _ptr(y_shared), _ptr(slot_of),
                              _ptr(topk_w), _ptr(out), _stream(stream)), "moe_combine")
@@ -357,7 +446,8 @@ def alloc_buffers(s: MoEShape, device="cuda", with_x_perm: bool = True) -> Layer
 @dataclass
 class LayerWeights:
     """Layer weights on the device; expert weights in the packed layout (bf16),
-    or FP8 codes with their row scales (``fp8``)."""
+    FP8 codes with their row scales (``fp8``), or 4-bit codes with their group
+    scales (``int4``: the group)."""
     w_router: torch.Tensor
     bias: Optional[torch.Tensor]
     w_gate_up: torch.Tensor       # E packed [2F, D] matrices (flat)
@@ -369,16 +459,19 @@ class LayerWeights:
     w_down_scale: Optional[torch.Tensor] = None       # FP8: [E, D]
     ws_gate_up_scale: Optional[torch.Tensor] = None   # FP8: [1, 2Fs]
     ws_down_scale: Optional[torch.Tensor] = None      # FP8: [1, D]
+    int4: int = 0                 # the group of 4-bit weights (scales [E, 2F, D / group], [E, D, F / group], ...)
 
 
 def upload_weights(s: MoEShape, w_router, bias, wgu, wd, shared, device="cuda",
-                   fp8: bool = False) -> LayerWeights:
+                   fp8: bool = False, int4: int = 0) -> LayerWeights:
     """Host arrays in storage encoding -> LayerWeights (expert weights packed on
-    the device, or quantised to FP8 there)."""
+    the device, or quantised there to FP8, or to 4 bits in groups of ``int4`` columns)."""
+    if fp8 and int4:
+        raise ValueError("fp8 and int4 exclude each other")
     td = lambda a: to_device(a, s, device)
     router = td(w_router)
     b = None if bias is None else torch.from_numpy(np.asarray(bias, np.float32)).to(device)
-    if not fp8:
+    if not fp8 and not int4:
         return LayerWeights(
             w_router=router, bias=b,
             w_gate_up=pack(td(wgu)),
@@ -386,22 +479,23 @@ def upload_weights(s: MoEShape, w_router, bias, wgu, wd, shared, device="cuda",
             ws_gate_up=None if shared is None else pack(td(shared[0])),
             ws_down=None if shared is None else pack(td(shared[1])),
         )
-    gu, gus = quantize_fp8(td(wgu))
-    dn, dns = quantize_fp8(td(wd))
+    quantize = quantize_fp8 if fp8 else lambda w: quantize_int4(w, int4)
+    gu, gus = quantize(td(wgu))
+    dn, dns = quantize(td(wd))
     sgu = sgus = sdn = sdns = None
     if shared is not None:
-        sgu, sgus = quantize_fp8(td(shared[0]))
-        sdn, sdns = quantize_fp8(td(shared[1]))
+        sgu, sgus = quantize(td(shared[0]))
+        sdn, sdns = quantize(td(shared[1]))
     return LayerWeights(w_router=router, bias=b, w_gate_up=gu, w_down=dn, ws_gate_up=sgu,
-                        ws_down=sdn, fp8=True, w_gate_up_scale=gus, w_down_scale=dns,
-                        ws_gate_up_scale=sgus, ws_down_scale=sdns)
+                        ws_down=sdn, fp8=fp8, w_gate_up_scale=gus, w_down_scale=dns,
+                        ws_gate_up_scale=sgus, ws_down_scale=sdns, int4=int4)
 
 
-def upload(inputs, device="cuda", fp8: bool = False):
+def upload(inputs, device="cuda", fp8: bool = False, int4: int = 0):
     """Seeded inputs (``inputs.LayerInputs``) -> (x, LayerWeights) on the device."""
     s = inputs.shape
     wgu, wd = inputs.all_experts()
-    w = upload_weights(s, inputs.w_router, inputs.bias, wgu, wd, inputs.shared(), device, fp8)
+    w = upload_weights(s, inputs.w_router, inputs.bias, wgu, wd, inputs.shared(), device, fp8, int4)
     return to_device(inputs.x, s, device), w
 
 
@@ -418,8 +512,13 @@ def layer_forward(s: MoEShape, x: torch.Tensor, w: LayerWeights, b: LayerBuffers
 
 
 def grouped_ffn(c: moe_shape, x: torch.Tensor, w: LayerWeights, b: LayerBuffers, stream=None):
-    """Both grouped GEMMs, with bf16 or FP8 expert weights."""
-    if w.fp8:
+    """Both grouped GEMMs, with bf16, FP8 or 4-bit expert weights."""
+    if w.int4:
+        moe_grouped_gate_up_int4(c, w.int4, b.x_perm, b.sorted_token, x, b.offsets, w.w_gate_up,
+                                 w.w_gate_up_scale, w.ws_gate_up, w.ws_gate_up_scale, b.h, stream)
+        moe_grouped_down_int4(c, w.int4, b.h, b.offsets, w.w_down, w.w_down_scale, w.ws_down, w.ws_down_scale,
+                              b.y_perm, b.y_shared, stream)
+    elif w.fp8:
         moe_grouped_gate_up_fp8(c, b.x_perm, b.sorted_token, x, b.offsets, w.w_gate_up,
                                 w.w_gate_up_scale, w.ws_gate_up, w.ws_gate_up_scale, b.h, stream)
         moe_grouped_down_fp8(c, b.h, b.offsets, w.w_down, w.w_down_scale, w.ws_down, w.ws_down_scale,
@@ -655,6 +754,18 @@ def _arg(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Opt
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}: "
                          f"{tuple(shape)} {dtype} on the device of the others is wanted")
+    if device < 0 or not t.is_contiguous():
+        _ptr(t)                                        # (raises)
+    return t.data_ptr()
+
+
+def _flat(t: Optional[torch.Tensor], numel: int, dtype, device: int, what: str) -> Optional[int]:
+    """Address of an argument of numel elements in any shape (on CUDA device `device`), or None."""
+    if t is None:
+        return None
+    if t.numel() != numel or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what} has {t.numel()} elements of {t.dtype} on {t.device}: "
+                         f"{numel} of {dtype} on the device of the others are wanted")
     if device < 0 or not t.is_contiguous():
         _ptr(t)                                        # (raises)
     return t.data_ptr()

@@ -5,6 +5,7 @@
 
 #include <cmath>
 
+#include "int4.h"
 #include "moe_internal.h"
 
 namespace {
@@ -390,6 +391,131 @@ int moe_grouped_down_fp8(const moe_shape* shape, const void* h, const int32_t* o
       s, static_cast<const moe::bf16_t*>(h), offsets, static_cast<const uint8_t*>(w_down),
       w_down_scale, static_cast<const uint8_t*>(ws_down), ws_down_scale,
       static_cast<moe::bf16_t*>(y_perm), static_cast<moe::bf16_t*>(y_shared), as_stream(stream)));
+}
+
+size_t moe_int4_packed_bytes(int64_t count, int32_t rows, int32_t cols) {
+  if (count < 0 || rows < 0 || cols < 0 || rows % 16 != 0 || cols % 128 != 0) return 0;
+  return static_cast<size_t>(count) * rows * (cols / 2);
+}
+
+namespace {
+
+int check_group(int32_t group) {
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_INVALID_ARG, "group = %d is not 32, 64 or 128", group);
+  return MOE_OK;
+}
+
+int check_int4_matrices(int64_t count, int32_t rows, int32_t cols) {
+  if (count < 0 || rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "negative count or size");
+  if (rows % 16 != 0 || cols % 128 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "rows = %d must be a multiple of 16 and cols = %d of 128", rows, cols);
+  if (rows > 0 && cols > 0 && count > (int64_t{1} << 48) / rows / cols)
+    return fail(MOE_ERR_UNSUPPORTED, "count * rows * cols > 2^48");
+  return MOE_OK;
+}
+
+int check_int4_call(const moe_shape* shape, int32_t group) {
+  if (int r = check_shape(shape)) return r;
+  if (shape->dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "4-bit weights need bf16 activations (dtype MOE_BF16)");
+  return check_group(group);
+}
+
+}  // namespace
+
+int moe_quantize_weights_int4(const void* w, void* w_int4, void* scales, int64_t count, int32_t rows,
+                              int32_t cols, int32_t group, void* stream) {
+  if (int r = check_group(group)) return r;
+  if (int r = check_int4_matrices(count, rows, cols)) return r;
+  if (count == 0 || rows == 0 || cols == 0) return ok();
+  NEED_PTR(w);
+  NEED_PTR(w_int4);
+  NEED_PTR(scales);
+  const size_t n = static_cast<size_t>(count) * rows * cols;
+  const Span out[] = {{w_int4, n / 2}, {scales, n / group * 2}}, in[] = {{w, n * 2}};
+  if (outputs_meet(out, in)) return fail(MOE_ERR_INVALID_ARG, "w, w_int4 and scales overlap");
+  return launched(moe::launch_quantize_int4(static_cast<const moe::bf16_t*>(w), static_cast<uint8_t*>(w_int4),
+                                            static_cast<moe::bf16_t*>(scales), count, rows, cols, group,
+                                            as_stream(stream)));
+}
+
+int moe_pack_weights_int4(const void* codes, void* w_int4, int64_t count, int32_t rows, int32_t cols,
+                          void* stream) {
+  if (int r = check_int4_matrices(count, rows, cols)) return r;
+  if (count == 0 || rows == 0 || cols == 0) return ok();
+  NEED_PTR(codes);
+  NEED_PTR(w_int4);
+  const size_t n = moe_int4_packed_bytes(count, rows, cols);
+  if (overlap(codes, n, w_int4, n)) return fail(MOE_ERR_INVALID_ARG, "codes and w_int4 overlap");
+  return launched(moe::launch_pack_int4(static_cast<const uint8_t*>(codes), static_cast<uint8_t*>(w_int4), count,
+                                        rows, cols, as_stream(stream)));
+}
+
+int moe_grouped_gate_up_int4(const moe_shape* shape, int32_t group, const void* x_perm,
+                             const int32_t* sorted_token, const void* x, const int32_t* offsets,
+                             const void* w_gate_up, const void* w_gate_up_scale, const void* ws_gate_up,
+                             const void* ws_gate_up_scale, void* h, void* stream) {
+  if (int r = check_int4_call(shape, group)) return r;
+  if (shape->T == 0) return ok();
+  OPT_PTR(x_perm);
+  if (x_perm == nullptr) NEED_PTR(sorted_token);
+  NEED_PTR(x);
+  NEED_PTR(offsets);
+  NEED_PTR(w_gate_up);
+  NEED_PTR(w_gate_up_scale);
+  if (shape->Fs > 0) {
+    NEED_PTR(ws_gate_up);
+    NEED_PTR(ws_gate_up_scale);
+  }
+  NEED_PTR(h);
+  const moe_shape& s = *shape;
+  const size_t rows = static_cast<size_t>(s.T) * s.k, bytes_x = static_cast<size_t>(s.T) * s.D * 2;
+  const size_t bytes_w = static_cast<size_t>(s.E) * 2 * s.F * s.D, bytes_ws = static_cast<size_t>(2) * s.Fs * s.D;
+  const Span out[] = {{h, (rows * s.F + static_cast<size_t>(s.T) * s.Fs) * 2}};
+  const Span in[] = {{x, bytes_x}, {x_perm, bytes_x * s.k}, {x_perm ? nullptr : sorted_token, rows * 4},
+                     {offsets, (static_cast<size_t>(s.E) + 1) * 4}, {w_gate_up, bytes_w / 2},
+                     {w_gate_up_scale, bytes_w / group * 2}, {s.Fs ? ws_gate_up : nullptr, bytes_ws / 2},
+                     {s.Fs ? ws_gate_up_scale : nullptr, bytes_ws / group * 2}};
+  if (outputs_meet(out, in)) return fail(MOE_ERR_INVALID_ARG, "h overlaps an input");
+  using moe::bf16_t;
+  return launched(moe::launch_gate_up_int4(
+      s, group, static_cast<const bf16_t*>(x_perm), sorted_token, static_cast<const bf16_t*>(x), offsets,
+      static_cast<const uint8_t*>(w_gate_up), static_cast<const bf16_t*>(w_gate_up_scale),
+      static_cast<const uint8_t*>(ws_gate_up), static_cast<const bf16_t*>(ws_gate_up_scale),
+      static_cast<bf16_t*>(h), as_stream(stream)));
+}
+
+int moe_grouped_down_int4(const moe_shape* shape, int32_t group, const void* h, const int32_t* offsets,
+                          const void* w_down, const void* w_down_scale, const void* ws_down,
+                          const void* ws_down_scale, void* y_perm, void* y_shared, void* stream) {
+  if (int r = check_int4_call(shape, group)) return r;
+  if (shape->T == 0) return ok();
+  NEED_PTR(h);
+  NEED_PTR(offsets);
+  NEED_PTR(w_down);
+  NEED_PTR(w_down_scale);
+  NEED_PTR(y_perm);
+  if (shape->Fs > 0) {
+    NEED_PTR(ws_down);
+    NEED_PTR(ws_down_scale);
+    NEED_PTR(y_shared);
+  }
+  const moe_shape& s = *shape;
+  const size_t rows = static_cast<size_t>(s.T) * s.k;
+  const size_t bytes_w = static_cast<size_t>(s.E) * s.D * s.F, bytes_ws = static_cast<size_t>(s.D) * s.Fs;
+  const Span out[] = {{y_perm, rows * s.D * 2}, {s.Fs ? y_shared : nullptr, static_cast<size_t>(s.T) * s.D * 2}};
+  const Span in[] = {{h, (rows * s.F + static_cast<size_t>(s.T) * s.Fs) * 2},
+                     {offsets, (static_cast<size_t>(s.E) + 1) * 4}, {w_down, bytes_w / 2},
+                     {w_down_scale, bytes_w / group * 2}, {s.Fs ? ws_down : nullptr, bytes_ws / 2},
+                     {s.Fs ? ws_down_scale : nullptr, bytes_ws / group * 2}};
+  if (outputs_meet(out, in)) return fail(MOE_ERR_INVALID_ARG, "y_perm, y_shared and the inputs overlap");
+  using moe::bf16_t;
+  return launched(moe::launch_down_int4(
+      s, group, static_cast<const bf16_t*>(h), offsets, static_cast<const uint8_t*>(w_down),
+      static_cast<const bf16_t*>(w_down_scale), static_cast<const uint8_t*>(ws_down),
+      static_cast<const bf16_t*>(ws_down_scale), static_cast<bf16_t*>(y_perm), static_cast<bf16_t*>(y_shared),
+      as_stream(stream)));
 }
 
 int moe_combine(const moe_shape* shape, const void* y_perm, const void* y_shared,
