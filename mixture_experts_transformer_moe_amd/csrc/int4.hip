@@ -23,6 +23,10 @@
 // (so that one mask takes out elements 2j and 2j + 1 as a bf16 pair).
 #include "int4.h"
 
+#include <type_traits>
+
+#include "grouped_gemm.h"
+
 namespace moe {
 namespace {
 
@@ -49,172 +53,286 @@ struct Int4Args {
   int ks_r, ks_s;            // waves of a workgroup that share a tile's reduction
 };
 
-// eight codes -> the bf16 operand 128 + code (element e from nibble e / 2 + 4 (e mod 2))
-__device__ __forceinline__ bf16x8 widen(uint32_t w) {
-  constexpr uint32_t kMask = 0x000f000fu, kBase = 0x43004300u;
-  const u32x4 v = {(w & kMask) | kBase, ((w >> 4) & kMask) | kBase, ((w >> 8) & kMask) | kBase,
-                   ((w >> 12) & kMask) | kBase};
-  return __builtin_bit_cast(bf16x8, v);
+// The constants of widen, one in a scalar and one in a vector register: an AND-OR
+// takes one of each, and with literals the compiler emits an AND and an OR.
+struct Widen {
+  uint32_t mask, base;
+  __device__ __forceinline__ Widen() : mask(0x000f000fu), base(0x43004300u) {
+    asm volatile("" : "+s"(mask));
+    asm volatile("" : "+v"(base));
+  }
+  // eight codes -> the bf16 operand 128 + code (element e from nibble e / 2 + 4 (e mod 2))
+  __device__ __forceinline__ bf16x8 operator()(uint32_t w) const {
+    const u32x4 v = {(w & mask) | base, ((w >> 4) & mask) | base, ((w >> 8) & mask) | base, ((w >> 12) & mask) | base};
+    return __builtin_bit_cast(bf16x8, v);
+  }
+};
+
+// 16 bytes at a base that is the same in every lane plus the lane's own offset.
+// The offset is made opaque where it is used: otherwise the compiler adds the two
+// outside the loop and holds a 64-bit address for every load.
+template <bool NT>
+__device__ __forceinline__ u32x4 load16(const void* base, uint32_t off) {
+  asm volatile("" : "+v"(off));
+  const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const unsigned char*>(base) + off);
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
 }
 
-// One workgroup: a column tile of one expert, its rows 16 TB at a time.  Four
+// One workgroup: a column tile of one expert, its rows up to 16 TM at a time.  Four
 // waves of 64 weight rows each (gate_up: 32 gate rows and the up rows of the same
-// columns): ks of them share the reduction, 4 / ks stand side by side.
-template <int MODE, int TB, int G>
-__global__ __launch_bounds__(256, TB <= 2 ? 3 : 2) void int4_rows_kernel(Int4Args a) {
+// columns): ks of them share the reduction, 4 / ks stand side by side.  Weights go
+// straight into registers, a block ahead; rows and scales are read as whole lines
+// and turned into operands through the wave's own LDS (read as operands they are
+// 16- and 2-byte pieces of many lines: 87 us against 75 for 32 tokens' gate/up at
+// D = 4096, F = 1024).  No barrier before the waves' parts meet.
+template <int MODE, int TM, int G>
+__global__ __launch_bounds__(256, TM == 1 ? 3 : (TM == 2 ? 2 : 1)) void int4_rows_kernel(Int4Args a) {
   constexpr int NB = 4;                                   // 16-row weight blocks of a wave
   constexpr int kCols = MODE == kInt4GateUp ? 32 : 64;    // output columns of a wave
   constexpr int GC = kColBlock / G;                       // groups of a packed block
-  __shared__ __attribute__((aligned(16))) float part[4 * NB * TB * 256];
+  constexpr int kAhead = TM == 2 ? 4 : 2;                 // blocks of weights in flight (TM 1: 2 and 3 workgroups a CU
+                                                          // beat 4 and 2 by 5% to 25%)
+  constexpr int kRun = 8;                                 // blocks whose scales are in LDS at a time
+  constexpr int NG = kRun * GC;                           // groups of a run
+  constexpr int kScaleLd = NG + 2;                        // (an odd number of words: no bank conflicts)
+  constexpr int kRowsBytes = 16 * TM * 2 * kColBlock;     // a block's columns of the rows
+  constexpr int kWaveBytes = kRowsBytes + 64 * kScaleLd * 2;
+  constexpr int kPartBytes = 4 * NB * TM * 256 * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char
+      smem[4 * kWaveBytes > kPartBytes ? 4 * kWaveBytes : kPartBytes];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // ---- whose tile: the shared expert's first, then those of the experts with rows
+  // ---- whose tile: chunk by chunk the shared expert's rows first, then each
+  // expert's.  Lane l counts the chunks of experts 4 l .. 4 l + 3.
+  constexpr int kChunk = 16 * TM;
   int bid = blockIdx.x;
-  const bool shared = bid < a.tiles_s;
-  int e = 0, lo = 0, M = a.T, tile = bid;
-  if (!shared) {
-    bid -= a.tiles_s;
-    int slot = bid / a.tiles_r;
+  const int chunks_s = a.tiles_s > 0 ? (a.T + kChunk - 1) / kChunk : 0;
+  const bool shared = bid < a.tiles_s * chunks_s;
+  int e = 0, lo = 0, M = a.T, tile, m0;
+  if (shared) {
+    m0 = bid / a.tiles_s * kChunk;
+    tile = bid % a.tiles_s;
+  } else {
+    bid -= a.tiles_s * chunks_s;
+    const int slot = bid / a.tiles_r;
     tile = bid % a.tiles_r;
-    e = -1;
-    for (int c = 0; c < a.E; c += 64) {
-      const int i = c + lane;
+    static_assert(kGemmMaxE == 4 * 64, "four experts a lane");
+    int off[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) off[j] = a.offsets[min(4 * lane + j, a.E)];
+    int sum = 0;
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
       // clamped so that no offsets table can move a row outside [0, S)
-      const int from = min(max(a.offsets[min(i, a.E)], 0), a.S);
-      const int to = min(max(a.offsets[min(i + 1, a.E)], from), a.S);
-      const bool has = i < a.E && to > from;
-      const uint64_t m = __ballot(has);
-      const int n = __popcll(m);
-      if (slot < n) {
-        const int rank = __popcll(m & ((uint64_t{1} << lane) - 1));
-        const int src = __ffsll(static_cast<unsigned long long>(__ballot(has && rank == slot))) - 1;
-        e = __builtin_amdgcn_readfirstlane(c + src);
-        lo = __builtin_amdgcn_readlane(from, src);
-        M = __builtin_amdgcn_readlane(to, src) - lo;
-        break;
-      }
-      slot -= n;
+      off[j] = min(max(off[j], j ? off[j - 1] : 0), a.S);
+      if (j) sum += (off[j] - off[j - 1] + kChunk - 1) / kChunk;
     }
-    if (e < 0) return;
+    int end = sum;                                        // inclusive scan
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(end, d);
+      if (lane >= d) end += v;
+    }
+    const uint64_t here = __ballot(slot < end);           // the first lane past the slot
+    if (here == 0) return;
+    const int src = __ffsll(static_cast<unsigned long long>(here)) - 1;
+    int left = slot - (end - sum), j = 0;                 // (of use in lane src)
+#pragma unroll
+    for (int q = 1; q < 4; ++q) {
+      const int n = (off[q] - off[q - 1] + kChunk - 1) / kChunk;
+      if (j == q - 1 && left >= n) {
+        left -= n;
+        j = q;
+      }
+    }
+    const int from = j == 0 ? off[0] : (j == 1 ? off[1] : (j == 2 ? off[2] : off[3]));
+    const int to = j == 0 ? off[1] : (j == 1 ? off[2] : (j == 2 ? off[3] : off[4]));
+    e = min(__builtin_amdgcn_readlane(4 * lane + j, src), a.E - 1);
+    lo = __builtin_amdgcn_readlane(from, src);
+    M = __builtin_amdgcn_readlane(to, src) - lo;
+    m0 = __builtin_amdgcn_readlane(left, src) * kChunk;
   }
   const int K = shared ? a.Ks : a.K;
   const int N = shared ? a.Ns : a.N;
   const int ks = shared ? a.ks_s : a.ks_r;
   const int rs = 4 / ks;
   const int Nw = MODE == kInt4GateUp ? 2 * N : N;
-  const int ncb = K / kColBlock;
+  const int ncb = K / kColBlock;                          // (even: K is a multiple of 256)
   const int kpart = wave % ks, side = wave / ks;
-  const int c0 = ncb * kpart / ks, c1 = ncb * (kpart + 1) / ks;
+  const int c0 = 2 * (ncb / 2 * kpart / ks), c1 = 2 * (ncb / 2 * (kpart + 1) / ks);
   const int n0 = (tile * rs + side) * kCols;
 
   // ---- weights and scales of the wave's four blocks
   const uint8_t* wmat = shared ? a.w_shared : a.w_routed + static_cast<size_t>(e) * Nw * (K / 2);
   const bf16_t* smat = shared ? a.s_shared : a.s_routed + static_cast<size_t>(e) * Nw * (K / G);
-  auto block_row = [&](int b) {
+  auto first_row = [&](int b) {                           // of weight block b
     return MODE == kInt4GateUp ? (b < 2 ? n0 + 16 * b : N + n0 + 16 * (b - 2)) : n0 + 16 * b;
   };
-  const uint8_t* wb[NB];
+  const uint8_t* wb[NB];                                  // (the same in every lane)
+  const bf16_t* sb[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    wb[b] = wmat + static_cast<size_t>(block_row(b) / kRowBlock) * ncb * kBlockBytes + lane * 16;
-  // lane l loads the scale of row l of the wave's 64
-  const int sb = lane >> 4;
-  const int srow = (MODE == kInt4GateUp ? (sb < 2 ? n0 + 16 * sb : N + n0 + 16 * (sb - 2)) : n0 + 16 * sb) + (lane & 15);
-  const bf16_t* sp = smat + static_cast<size_t>(srow) * (K / G);
+  for (int b = 0; b < NB; ++b) {
+    wb[b] = wmat + static_cast<size_t>(first_row(b) / kRowBlock) * ncb * kBlockBytes;
+    sb[b] = smat + static_cast<size_t>(first_row(b)) * (K / G);
+  }
+  unsigned char* my_rows = smem + wave * kWaveBytes;
+  uint32_t* my_scales = reinterpret_cast<uint32_t*>(my_rows + kRowsBytes);
 
-  struct Buf {
-    u32x4 w[NB];
-    u32x4 x[TB][4];
-    uint16_t s[GC];
+  // the scales of the wave's 64 rows and a run of 8 blocks, two groups a word: word
+  // i of a run holds groups 2 (i mod kP) .. + 1 of row i / kP
+  constexpr int kP = NG / 2;
+  struct Run {
+    uint32_t v[kP];
+  };
+  auto load_run = [&](Run& r, int cs) __attribute__((always_inline)) {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));                          // (the addresses are not kept in registers)
+    const int word = min(ln % kP, (c1 - cs) * GC / 2 - 1);  // inside the wave's part
+    const uint32_t off = (static_cast<uint32_t>(ln / kP) * static_cast<uint32_t>(K / G) + 2u * word) * 2u;
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      constexpr int kRows = 64 / kP;                      // rows of a load
+      const bf16_t* from = sb[j * kRows / 16] + (j * kRows % 16) * (K / G) + cs * GC;
+      r.v[j] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const unsigned char*>(from) + off);
+    }
+  };
+  auto keep_run = [&](const Run& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kP; ++j) my_scales[(j * (64 / kP) + lane / kP) * (kScaleLd / 2) + lane % kP] = r.v[j];
   };
 
-  for (int m0 = 0; m0 < M; m0 += 16 * TB) {
-    const bf16_t* xr[TB];
+  // rows m0 .. m0 + 4 NI - 1
+  auto chunk = [&](auto ni_tag) __attribute__((always_inline)) {
+    constexpr int NI = decltype(ni_tag)::value;
+    int lane = tid & 63;
+    asm volatile("" : "+v"(lane));      // per-lane arithmetic stays inside its variant
+    constexpr int TB = (NI + 3) / 4;                      // token blocks of 16
+    u32x4 ring[kAhead][NB];                               // weights of the next blocks
+    u32x4 rows[NI];                                       // the next block's, on their way to LDS
+    // load i: row 4 i + lane / 16, its 16-byte piece lane mod 16 of a block's 256
+    // bytes; in LDS piece c of row r sits at slot c ^ (r mod 16) (no bank conflicts
+    // either way)
+    const bf16_t* base = shared ? a.a_shared + static_cast<size_t>(m0) * K
+                                : (a.gather ? a.a_routed : a.a_routed + static_cast<size_t>(lo + m0) * K);
+    uint32_t xo[NI];
+    int tok[NI];
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-      const int m = min(m0 + 16 * t + (lane & 15), M - 1);
-      const bf16_t* base = a.a_shared;
-      int row = m;
-      if (!shared) {
-        base = a.a_routed;
-        row = lo + m;
-        if (a.gather) row = min(max(a.gather[row], 0), a.T - 1);
-      }
-      xr[t] = base + static_cast<size_t>(row) * K + 8 * (lane >> 4);
+    for (int i = 0; i < NI; ++i) {
+      const int row = min(4 * i + (lane >> 4), M - 1 - m0);
+      tok[i] = !shared && a.gather ? a.gather[lo + m0 + row] : row;
     }
+    const Widen widen;
     f32x4 acc[TB][NB];
 #pragma unroll
     for (int t = 0; t < TB; ++t)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto load = [&](Buf& f, int cb) __attribute__((always_inline)) {
+    auto load = [&](u32x4 (&w)[NB], int cb) __attribute__((always_inline)) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        f.w[b] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wb[b] + static_cast<size_t>(cb) * kBlockBytes));
+        w[b] = load16<true>(wb[b] + static_cast<size_t>(cb < c1 ? cb : c0) * kBlockBytes, cb < c1 ? lane * 16u : 0u);
+    };
+    auto load_rows = [&](int cb) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) rows[i] = load16<false>(base + (cb < c1 ? cb : c0) * kColBlock, cb < c1 ? xo[i] : 0u);
+    };
+    auto keep_rows = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = 4 * i + (lane >> 4);
+        *reinterpret_cast<u32x4*>(my_rows + r * 256 + (((lane & 15) ^ (r & 15)) << 4)) = rows[i];
+      }
+    };
+    auto compute = [&](const u32x4 (&wq)[NB], int j, bool odd) __attribute__((always_inline)) {   // block j of the run
+      constexpr int SG = 4 / GC;                         // MFMA steps of a group
+      const u32x4 offset = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};   // -136
+      // (a wave's LDS operations are done in order; tokens past 4 NI - 1 hold what
+      // was there, and only outputs that are not stored depend on them)
+      bf16x8 x[TB][4];
 #pragma unroll
       for (int t = 0; t < TB; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          f.x[t][i] = *reinterpret_cast<const u32x4*>(xr[t] + cb * kColBlock + 32 * i);
-#pragma unroll
-      for (int g = 0; g < GC; ++g) f.s[g] = sp[cb * GC + g];
-    };
-    auto compute = [&](const Buf& f) __attribute__((always_inline)) {
-      constexpr int SG = 4 / GC;                         // MFMA steps of a group
-      const u32x4 offset = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};   // -136
+          x[t][i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
+                                                   my_rows + (16 * t + (lane & 15)) * 256 +
+                                                   (((4 * i + (lane >> 4)) ^ (lane & 15)) << 4)));
 #pragma unroll
       for (int g = 0; g < GC; ++g) {
-        // the scales of rows l mod 16 of each block, from the lanes that loaded them
-        const uint32_t own = static_cast<uint32_t>(f.s[g]) << 16;
+        // the scale of row `lane` of the wave's 64, then those of rows lane mod 16
+        // of each block
+        const uint32_t two = my_scales[lane * (kScaleLd / 2) + (j * GC + g) / 2];
+        const uint32_t own = (GC == 1 ? odd : g % 2 != 0) ? two & 0xffff0000u : two << 16;
         const auto p = __builtin_amdgcn_permlane32_swap(own, own, false, false);       // rows 0 1 0 1, 2 3 2 3
         const auto p01 = __builtin_amdgcn_permlane16_swap(p[0], p[0], false, false);
         const auto p23 = __builtin_amdgcn_permlane16_swap(p[1], p[1], false, false);
         const float sc[NB] = {__uint_as_float(p01[0]), __uint_as_float(p01[1]), __uint_as_float(p23[0]),
                               __uint_as_float(p23[1])};
-        f32x4 base[TB];
+        f32x4 start[TB];
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
-          base[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          start[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < SG; ++i)
-            base[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.x[t][g * SG + i]),
-                                                               __builtin_bit_cast(bf16x8, offset), base[t], 0, 0, 0);
+            start[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][g * SG + i], __builtin_bit_cast(bf16x8, offset),
+                                                                start[t], 0, 0, 0);
         }
+        // a step of all blocks at a time: NB TB chains side by side
+        f32x4 y[TB][NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          bf16x8 w[SG];
+        for (int i = 0; i < SG; ++i) {
 #pragma unroll
-          for (int i = 0; i < SG; ++i) w[i] = widen(f.w[b][g * SG + i]);
+          for (int b = 0; b < NB; ++b) {
+            const bf16x8 w = widen(wq[b][g * SG + i]);
 #pragma unroll
-          for (int t = 0; t < TB; ++t) {
-            f32x4 y = base[t];
-#pragma unroll
-            for (int i = 0; i < SG; ++i)
-              y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.x[t][g * SG + i]), w[i], y, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[t][b][r] = fmaf(sc[b], y[r], acc[t][b][r]);
+            for (int t = 0; t < TB; ++t)
+              y[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][g * SG + i], w, i == 0 ? start[t] : y[t][b], 0, 0, 0);
           }
+          __builtin_amdgcn_sched_barrier(0);              // a step's operands at a time
         }
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[t][b][r] = fmaf(sc[b], y[t][b][r], acc[t][b][r]);
       }
     };
-    // two buffers; the loads are unconditional (the last repeats a block), so that
-    // the waits before each block leave the next one's loads in flight
+    // kAhead blocks of weights in flight; the loads are unconditional (past the end
+    // every lane reads the same 16 bytes), so that the waits before a block leave
+    // those of the later ones in flight
     if (c0 < c1) {
-      Buf f0, f1;
-      load(f0, c0);
-      for (int cb = c0;;) {
-        load(f1, min(cb + 1, c1 - 1));
-        compute(f0);
-        if (++cb >= c1) break;
-        load(f0, min(cb + 1, c1 - 1));
-        compute(f1);
-        if (++cb >= c1) break;
+      Run run;
+      load_run(run, c0);
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) load(ring[q], c0 + q);
+      __builtin_amdgcn_sched_barrier(0);                  // the weights are under way before the rows' ids are here
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int row = !shared && a.gather ? min(max(tok[i], 0), a.T - 1) : tok[i];
+        xo[i] = (static_cast<uint32_t>(row) * static_cast<uint32_t>(K) + 8u * (lane & 15)) * 2u;
+      }
+      load_rows(c0);
+      for (int cb = c0; cb < c1; cb += kAhead) {
+        if ((cb - c0) % kRun == 0) {
+          keep_run(run);
+          load_run(run, min(cb + kRun, c1 - 2));
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          keep_rows();
+          load_rows(cb + q + 1);
+          if (cb + q < c1) compute(ring[q], (cb - c0) % kRun + q, q % 2 != 0);
+          load(ring[q], cb + q + kAhead);
+        }
       }
     }
 
     // ---- the waves' parts meet in LDS: [wave][tb][block][token][row]
+    float* part = reinterpret_cast<float*>(smem);
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < TB; ++t)
 #pragma unroll
@@ -223,11 +341,11 @@ __global__ __launch_bounds__(256, TB <= 2 ? 3 : 2) void int4_rows_kernel(Int4Arg
         for (int r = 0; r < 4; ++r)
           part[((wave * TB + t) * NB + b) * 256 + (4 * (lane >> 4) + r) * 16 + (lane & 15)] = acc[t][b][r];
     __syncthreads();
-    const int pairs = kCols / 2;                          // column pairs of a side
-    for (int i = tid; i < rs * 16 * TB * pairs; i += 256) {
-      const int c = 2 * (i % pairs), rest = i / pairs;
-      const int m = rest % (16 * TB), sd = rest / (16 * TB);
-      if (m0 + m >= M) continue;
+    constexpr int kPairs = kCols / 2;                     // column pairs of a side
+    const int left = min(M - m0, 4 * NI);
+    for (int i = tid; i < rs * left * kPairs; i += 256) {
+      const int c = 2 * (i % kPairs), rest = i / kPairs;
+      const int m = rest % left, sd = rest / left;
       auto sum = [&](int b, int r) {
         float v = 0.f;
         for (int k = 0; k < ks; ++k)
@@ -248,8 +366,13 @@ __global__ __launch_bounds__(256, TB <= 2 ? 3 : 2) void int4_rows_kernel(Int4Arg
       *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(m0 + m) * N + (tile * rs + sd) * kCols + c) =
           pack_bf16x2(y[0], y[1]);
     }
-    __syncthreads();
-  }
+  };
+  // with as few row loads as hold the chunk
+  const int left = M - m0;
+  if (TM > 2 && left > 32) chunk(std::integral_constant<int, 4 * TM>{});
+  else if (TM > 1 && left > 16) chunk(std::integral_constant<int, (TM > 1 ? 8 : 4)>{});
+  else if (left > 4) chunk(std::integral_constant<int, 4>{});
+  else chunk(std::integral_constant<int, 1>{});
 }
 
 // ------------------------------------------------------------------ load time
@@ -321,39 +444,47 @@ __global__ __launch_bounds__(256) void quantize_int4_kernel(const bf16_t* __rest
   }
 }
 
-template <int MODE, int G>
-hipError_t launch_rows(Int4Args a, int slots, int tb, hipStream_t st) {
-  constexpr int kCols = MODE == kInt4GateUp ? 32 : 64;
-  const unsigned grid = static_cast<unsigned>(a.tiles_s) + static_cast<unsigned>(slots) * a.tiles_r;
-  (void)kCols;
-  if (grid == 0) return hipSuccess;
-  if (tb == 1) int4_rows_kernel<MODE, 1, G><<<grid, 256, 0, st>>>(a);
-  else if (tb == 2) int4_rows_kernel<MODE, 2, G><<<grid, 256, 0, st>>>(a);
-  else int4_rows_kernel<MODE, 4, G><<<grid, 256, 0, st>>>(a);
-  return hipGetLastError();
-}
-
-template <int MODE>
-hipError_t launch_int4(Int4Args a, const moe_shape& s, int group, hipStream_t st) {
-  constexpr int kCols = MODE == kInt4GateUp ? 32 : 64;
-  const int slots = a.S < a.E ? a.S : a.E;
-  // waves that share a reduction: one, unless too few workgroups would be left
-  auto split = [&](int K, int N, int groups) {
+template <int MODE, int TM>
+hipError_t launch_rows(Int4Args a, int group, hipStream_t st) {
+  constexpr int kCols = MODE == kInt4GateUp ? 32 : 64, kChunk = 16 * TM;
+  // chunks the experts' rows can make
+  const int64_t most = static_cast<int64_t>(a.E) + a.S / kChunk;
+  const int64_t slots = a.S < most ? a.S : most;
+  // Waves that share a reduction.  More of them make more workgroups of the same
+  // rows, which evens out their last round; each costs a start (offsets, row ids,
+  // first loads: 4 to 6 us, beside the others').  So up to 4096 workgroups as long
+  // as a wave keeps 8 blocks (32 tokens, D = 4096, F = 1024: gate/up 64 us split in
+  // 2, 69 whole; down, K = 1024, 38 split, 36 whole), and up to 1024 at any length.
+  auto split = [&](int K, int N, int64_t chunks) {
     int ks = 1;
-    while (ks < 4 && K / kColBlock >= 4 * ks && static_cast<int64_t>(groups) * (N / (kCols * (4 / ks))) < 2048) ks *= 2;
+    for (; ks < 4; ks *= 2) {
+      const int64_t groups = chunks * (N / (kCols * (4 / ks)));
+      const int blocks = K / kColBlock / (2 * ks);        // of a wave after one more split
+      if (!(blocks >= 8 && groups < 4096) && !(blocks >= 2 && groups < 1024)) break;
+    }
     return ks;
   };
   a.ks_r = split(a.K, a.N, slots);
   a.tiles_r = a.N / (kCols * (4 / a.ks_r));
-  a.ks_s = a.Ns > 0 ? split(a.Ks, a.Ns, 1) : 1;
+  const int64_t chunks_s = (a.T + kChunk - 1) / kChunk;
+  a.ks_s = a.Ns > 0 ? split(a.Ks, a.Ns, chunks_s) : 1;
   a.tiles_s = a.Ns > 0 ? a.Ns / (kCols * (4 / a.ks_s)) : 0;
-  const int mean = a.S / a.E;
-  const int tb = mean >= 48 ? 4 : (mean >= 8 || s.T > 16 ? 2 : 1);
+  const int64_t grid = a.tiles_s * chunks_s + slots * a.tiles_r;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
   switch (group) {
-    case 32: return launch_rows<MODE, 32>(a, slots, tb, st);
-    case 64: return launch_rows<MODE, 64>(a, slots, tb, st);
-    default: return launch_rows<MODE, 128>(a, slots, tb, st);
+    case 32: int4_rows_kernel<MODE, TM, 32><<<static_cast<unsigned>(grid), 256, 0, st>>>(a); break;
+    case 64: int4_rows_kernel<MODE, TM, 64><<<static_cast<unsigned>(grid), 256, 0, st>>>(a); break;
+    default: int4_rows_kernel<MODE, TM, 128><<<static_cast<unsigned>(grid), 256, 0, st>>>(a); break;
   }
+  return hipGetLastError();
+}
+
+template <int MODE>
+hipError_t launch_int4(const Int4Args& a, int group, hipStream_t st) {
+  const int mean = a.S / a.E;
+  if (mean >= 32) return launch_rows<MODE, 4>(a, group, st);
+  if (mean >= 12) return launch_rows<MODE, 2>(a, group, st);
+  return launch_rows<MODE, 1>(a, group, st);
 }
 
 int grid_for(int64_t items) {
@@ -401,7 +532,7 @@ hipError_t launch_gate_up_int4(const moe_shape& s, int group, const bf16_t* x_pe
   a.K = a.Ks = s.D;
   a.N = s.F;
   a.Ns = s.Fs;
-  return launch_int4<kInt4GateUp>(a, s, group, st);
+  return launch_int4<kInt4GateUp>(a, group, st);
 }
 
 hipError_t launch_down_int4(const moe_shape& s, int group, const bf16_t* h, const int32_t* offsets,
@@ -424,7 +555,7 @@ hipError_t launch_down_int4(const moe_shape& s, int group, const bf16_t* h, cons
   a.Ks = s.Fs;
   a.N = s.D;
   a.Ns = s.Fs > 0 ? s.D : 0;
-  return launch_int4<kInt4Down>(a, s, group, st);
+  return launch_int4<kInt4Down>(a, group, st);
 }
 
 }  // namespace moe
