@@ -588,6 +588,53 @@ int moe_orthogonalize(int64_t count, int32_t rows, int32_t cols, int32_t dtype, 
                       float* momentum, float mu, int32_t nesterov, int32_t steps, float eps, float scale,
                       void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The training step's loss: softmax cross entropy of the output head over its
+ * vocabulary ("Laguna-M.1-base", Shape: vocabulary of 100352), without the logits
+ * in memory.  For hidden states x [rows, cols], the head's weights w [vocab, cols]
+ * and targets y:
+ *   z[t, v] = x_t w_v;  lse_t = log sum_v exp z[t, v];  loss_t = lse_t - z[t, y_t]
+ *   P[t, v] = (exp(z[t, v] - lse_t) - [v = y_t]) dloss_t;  dx = P w;  dw = P^T x
+ * A row whose target is outside 0 .. vocab - 1 takes no part (padding, ignored
+ * positions): its loss and lse are 0, its dx is 0, nothing of it is in dw, and what
+ * stands in its x, lse and dloss does not matter, not even infinities and NaN.
+ * dtype MOE_BF16 only (MOE_ERR_UNSUPPORTED otherwise), products with fp32
+ * accumulation, statistics in fp32.  cols % 8 == 0, any rows >= 0 and vocab >= 1;
+ * rows < 2^22, cols <= 65536, vocab < 2^23, rows * vocab < 2^38 (else
+ * MOE_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of workspace both calls need (0 for sizes they reject, and for rows == 0). */
+size_t moe_head_loss_workspace_bytes(int64_t rows, int32_t cols, int32_t vocab);
+
+/* Forward.
+ *   x       [rows, cols] bf16;  w [vocab, cols] bf16, row-major;  target [rows] int32
+ *   loss    [rows] fp32 out
+ *   lse     [rows] fp32 out, what the backward pass needs
+ *   workspace >= moe_head_loss_workspace_bytes bytes
+ * A row with a logit that is not finite has a loss that is not finite (or, where
+ * the logit is -infinity and not the target's, counts it as probability 0).
+ * Outputs must not overlap the other arguments. */
+int moe_head_loss_forward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,
+                          const int32_t* target, float* loss, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Gradients of sum_t dloss_t loss_t.
+ *   lse     [rows] fp32 from the forward pass
+ *   dloss   [rows] fp32: the gradient that arrives at each row's loss (1 / N for a
+ *           mean over N rows)
+ *   dx      [rows, cols] bf16 out;  dw [vocab, cols] bf16 out; either may be NULL
+ *           (not computed), not both
+ *   workspace as for the forward pass
+ * The vocabulary goes by in pieces, each piece's logits computed again.  P is
+ * rounded to bf16 for the two products, dx and dw once more.  All sums run in a
+ * fixed order: the results are bit-reproducible.  rows == 0 writes zeros to dw.
+ * Outputs must not overlap the other arguments.  The workspace holds nothing between
+ * calls; calls and captured graphs that may run at the same time need one each. */
+int moe_head_loss_backward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,
+                           const int32_t* target, const float* lse, const float* dloss, void* dx, void* dw,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

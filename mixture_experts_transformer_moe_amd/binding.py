@@ -36,7 +36,8 @@ EXPORTS = ("moe_version", "moe_status_string", "moe_last_error", "moe_workspace_
            "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward",
            "moe_orthogonalize_workspace_bytes", "moe_orthogonalize",
            "moe_int4_packed_bytes", "moe_quantize_weights_int4", "moe_pack_weights_int4",
-           "moe_grouped_gate_up_int4", "moe_grouped_down_int4")
+           "moe_grouped_gate_up_int4", "moe_grouped_down_int4",
+           "moe_head_loss_workspace_bytes", "moe_head_loss_forward", "moe_head_loss_backward")
 
 
 class moe_shape(ctypes.Structure):
@@ -151,6 +152,13 @@ def lib() -> ctypes.CDLL:
         L.moe_grouped_gate_up_int4.argtypes = [_SP, i32] + [_P] * 10
         L.moe_grouped_down_int4.restype = ctypes.c_int
         L.moe_grouped_down_int4.argtypes = [_SP, i32] + [_P] * 9
+        # the head's loss
+        L.moe_head_loss_workspace_bytes.restype = size
+        L.moe_head_loss_workspace_bytes.argtypes = [i64, i32, i32]
+        L.moe_head_loss_forward.restype = ctypes.c_int
+        L.moe_head_loss_forward.argtypes = [i64, i32, i32, i32] + [_P] * 6 + [size, _P]
+        L.moe_head_loss_backward.restype = ctypes.c_int
+        L.moe_head_loss_backward.argtypes = [i64, i32, i32, i32] + [_P] * 8 + [size, _P]
         _lib = L
     return _lib
 
@@ -845,3 +853,41 @@ def moe_orthogonalize(g, momentum, mu, nesterov, steps, eps, scale, out, workspa
     _check(lib().moe_orthogonalize(
         count, rows, cols, _elem(g, "g"), _ptr(g), mo, mu, int(bool(nesterov)), steps, eps, scale, to,
         _workspace_arg(workspace, dev), _nbytes(workspace), _stream_on(stream, dev)), "moe_orthogonalize")
+
+
+# ---------------------------------------------------------------------------
+# the training step's loss: the output head's cross entropy
+# ---------------------------------------------------------------------------
+
+def moe_head_loss_workspace_bytes(rows, cols, vocab) -> int:
+    return int(lib().moe_head_loss_workspace_bytes(int(rows), int(cols), int(vocab)))
+
+
+def _head_args(x, w, target):
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [rows, cols] and w [vocab, cols]")
+    (rows, cols), dev = x.shape, x.get_device()
+    vocab = w.shape[0]
+    return rows, cols, vocab, dev, _arg(w, (vocab, cols), x.dtype, dev, "w"), _arg(target, (rows,), torch.int32, dev,
+                                                                                 "target")
+
+
+def moe_head_loss_forward(x, w, target, loss, lse, workspace, stream=None):
+    """Cross entropy of x [rows, cols] under the head w [vocab, cols]; targets outside the vocabulary take no part."""
+    rows, cols, vocab, dev, wp, tp = _head_args(x, w, target)
+    f32 = torch.float32
+    _check(lib().moe_head_loss_forward(
+        rows, cols, vocab, _elem(x, "x"), _ptr(x), wp, tp, _arg(loss, (rows,), f32, dev, "loss"),
+        _arg(lse, (rows,), f32, dev, "lse"), _workspace_arg(workspace, dev), _nbytes(workspace),
+        _stream_on(stream, dev)), "moe_head_loss_forward")
+
+
+def moe_head_loss_backward(x, w, target, lse, dloss, dx, dw, workspace, stream=None):
+    """Gradients of sum(dloss * loss); dx or dw may be None."""
+    rows, cols, vocab, dev, wp, tp = _head_args(x, w, target)
+    f32 = torch.float32
+    _check(lib().moe_head_loss_backward(
+        rows, cols, vocab, _elem(x, "x"), _ptr(x), wp, tp, _arg(lse, (rows,), f32, dev, "lse"),
+        _arg(dloss, (rows,), f32, dev, "dloss"), _arg(dx, (rows, cols), x.dtype, dev, "dx"),
+        _arg(dw, (vocab, cols), x.dtype, dev, "dw"), _workspace_arg(workspace, dev), _nbytes(workspace),
+        _stream_on(stream, dev)), "moe_head_loss_backward")

@@ -5,6 +5,7 @@
 
 #include <cmath>
 
+#include "head_loss.h"
 #include "int4.h"
 #include "moe_internal.h"
 
@@ -889,6 +890,79 @@ int moe_orthogonalize(int64_t count, int32_t rows, int32_t cols, int32_t dtype, 
     return fail(MOE_ERR_INVALID_ARG, "g, momentum, out and workspace overlap");
   return launched(moe::launch_orthogonalize(count, rows, cols, bf16, g, momentum, mu, nesterov != 0, steps, eps,
                                             scale, static_cast<moe::bf16_t*>(out), workspace, as_stream(stream)));
+}
+
+// ------------------------------------------------------------ the head's loss
+
+namespace {
+
+int check_head(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype) {
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %lld < 0", static_cast<long long>(rows));
+  if (cols < 1 || vocab < 1) return fail(MOE_ERR_INVALID_ARG, "cols = %d, vocab = %d: at least 1", cols, vocab);
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "dtype %d is neither MOE_F32 nor MOE_BF16", dtype);
+  if (dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "the head's loss is bf16 only");
+  if (cols % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "cols = %d is not a multiple of 8", cols);
+  if (rows >= (1 << 22) || cols > 65536 || vocab >= (1 << 23))
+    return fail(MOE_ERR_UNSUPPORTED, "rows = %lld (below 2^22), cols = %d (to 65536), vocab = %d (below 2^23)",
+                static_cast<long long>(rows), cols, vocab);
+  if (rows * vocab >= (int64_t{1} << 38)) return fail(MOE_ERR_UNSUPPORTED, "rows * vocab >= 2^38");
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_head_loss_workspace_bytes(int64_t rows, int32_t cols, int32_t vocab) {
+  if (check_head(rows, cols, vocab, MOE_BF16) != MOE_OK || rows == 0) return 0;
+  return moe::head_loss_workspace_bytes(rows, cols, vocab);
+}
+
+int moe_head_loss_forward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,
+                          const int32_t* target, float* loss, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (int r = check_head(rows, cols, vocab, dtype)) return r;
+  if (rows == 0) return ok();
+  NEED_PTR(x);
+  NEED_PTR(w);
+  NEED_PTR(target);
+  NEED_PTR(loss);
+  NEED_PTR(lse);
+  const size_t need = moe::head_loss_workspace_bytes(rows, cols, vocab);
+  if (int r = check_workspace(workspace, workspace_bytes, need)) return r;
+  const size_t n = static_cast<size_t>(rows), d = static_cast<size_t>(cols);
+  const Span out[] = {{loss, n * 4}, {lse, n * 4}, {workspace, need}};
+  const Span in[] = {{x, n * d * 2}, {w, vocab * d * 2}, {target, n * 4}};
+  if (outputs_meet(out, in)) return fail(MOE_ERR_INVALID_ARG, "loss, lse, workspace and the inputs overlap");
+  return launched(moe::launch_head_loss_forward(static_cast<int>(rows), cols, vocab, static_cast<const moe::bf16_t*>(x),
+                                                static_cast<const moe::bf16_t*>(w), target, loss, lse, workspace,
+                                                as_stream(stream)));
+}
+
+int moe_head_loss_backward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,
+                           const int32_t* target, const float* lse, const float* dloss, void* dx, void* dw,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (int r = check_head(rows, cols, vocab, dtype)) return r;
+  OPT_PTR(dx);
+  OPT_PTR(dw);
+  if (dx == nullptr && dw == nullptr) return fail(MOE_ERR_INVALID_ARG, "dx and dw are both NULL");
+  if (rows > 0) {
+    NEED_PTR(x);
+    NEED_PTR(w);
+    NEED_PTR(target);
+    NEED_PTR(lse);
+    NEED_PTR(dloss);
+    const size_t need = moe::head_loss_workspace_bytes(rows, cols, vocab);
+    if (int r = check_workspace(workspace, workspace_bytes, need)) return r;
+    const size_t n = static_cast<size_t>(rows), d = static_cast<size_t>(cols);
+    const Span out[] = {{dx, n * d * 2}, {dw, vocab * d * 2}, {workspace, need}};
+    const Span in[] = {{x, n * d * 2}, {w, vocab * d * 2}, {target, n * 4}, {lse, n * 4}, {dloss, n * 4}};
+    if (outputs_meet(out, in)) return fail(MOE_ERR_INVALID_ARG, "dx, dw, workspace and the inputs overlap");
+  } else if (dw == nullptr) {
+    return ok();
+  }
+  return launched(moe::launch_head_loss_backward(
+      static_cast<int>(rows), cols, vocab, static_cast<const moe::bf16_t*>(x), static_cast<const moe::bf16_t*>(w),
+      target, lse, dloss, static_cast<moe::bf16_t*>(dx), static_cast<moe::bf16_t*>(dw), workspace, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,548 @@
+// Softmax cross entropy of the output head over a large vocabulary, without its
+// logits, and the gradients of the hidden states and of the head's weights
+// ("Laguna-M.1-base", Shape: vocabulary of 100352; the training step whose other
+// end is the update).
+//
+//   z[t, v] = x_t w_v;  lse_t = log sum_v exp z[t, v];  loss_t = lse_t - z[t, y_t]
+//   P[t, v] = (exp(z[t, v] - lse_t) - [v = y_t]) g_t;  dx = P W;  dW = P^T x
+// A row whose target is outside the vocabulary takes no part.
+//
+// Forward: a tile of z stays in the accumulators; each row's maximum and sum over
+// the tile's columns go out (8 bytes for 256 columns) and a second kernel joins
+// them in a fixed order.  Backward: the vocabulary goes by in pieces; per piece z
+// is computed again, P leaves the accumulators once as bf16, row-major both ways
+// (P for dx, its transpose for dW), and two products follow.  W's piece and x are
+// transposed beside it, so that every product is the same kernel's form (gemm_nt.h:
+// both operands along the reduction).  dx is summed over pieces in fp32.
+// P in bf16 is the one rounding inside (2^-9 of an entry on average, independent
+// from entry to entry: 1.1e-3 of the gradients' norm beside their own rounding's
+// 1.7e-3); an entry of the target is p - 1 from fp32.
+#include "head_loss.h"
+
+#include "gemm_nt.h"
+
+namespace moe {
+namespace {
+
+typedef __attribute__((address_space(1))) unsigned char gbyte;
+typedef __attribute__((address_space(1))) u32x4 gu32x4;
+
+// row blocks by the rows of the batch: 256 x 256 tiles, and narrower ones that
+// leave small batches bound by the weights
+using Wide = NtShape<2, 2, 4, 4>;
+using Rows128 = NtShape<1, 4, 4, 2>;
+using Rows64 = NtShape<1, 4, 2, 2>;
+using Rows32 = NtShape<1, 4, 1, 2>;
+
+// The bf16 tile of a wave (32 MB rows, 32 NB columns; value(m, n, r) gives register
+// r of block (m, n), rounded) through its LDS, stored as whole row segments: rows
+// below `rows`, columns below `cols` (whole pieces of 8).
+template <class S, class F>
+__device__ __forceinline__ void store_rows(bf16_t* out, size_t ld, int rows, int cols, unsigned char* stg, F&& value) {
+  const int lane = threadIdx.x & 63;
+  constexpr int kPieces = 4 * S::NB;                       // 16-byte pieces of a row
+  constexpr int kRowB = 16 * kPieces;
+  auto swz = [](int r) { return S::NB == 4 ? r & 15 : (r >> 1) & 7; };
+#pragma unroll
+  for (int m = 0; m < S::MB; ++m) {
+#pragma unroll
+    for (int n = 0; n < S::NB; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = lane & 31, c = 4 * n + q;
+        uint2 v;
+        v.x = pack_bf16x2(value(m, n, 4 * q), value(m, n, 4 * q + 1));
+        v.y = pack_bf16x2(value(m, n, 4 * q + 2), value(m, n, 4 * q + 3));
+        *reinterpret_cast<uint2*>(stg + r * kRowB + ((c ^ swz(r)) << 4) + 8 * (lane >> 5)) = v;
+      }
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kPieces / 2; ++i) {                // 64 pieces a store
+      const int at = 64 * i + lane, r = at / kPieces, c = at % kPieces;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(stg + r * kRowB + ((c ^ swz(r)) << 4));
+      if (32 * m + r < rows && 8 * c < cols)
+        *(gu32x4*)((gbyte*)(out + static_cast<size_t>(32 * m + r) * ld + 8 * c)) = v;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+struct LogitArgs {
+  const bf16_t* x;          // [T, D]
+  const bf16_t* w;          // [V, D]
+  const int32_t* target;    // [T]
+  int T, D, V;
+  int v0, v1;               // the columns of this launch
+  int tiles_m, tiles_n;
+  // forward
+  float2* part;             // [T, parts]: maximum and sum of each column tile
+  int parts;
+  float* zt;                // [T]: the target's logit
+  // backward
+  const float* lse;
+  const float* dloss;
+  bf16_t* p;                // [T, ldp]
+  bf16_t* pt;               // [v1 - v0, ldt]
+  int ldp, ldt;
+};
+
+template <class S>
+__device__ __forceinline__ void logits_tile(const LogitArgs& g, unsigned char* smem, int& t0, int& v0, f32x16 (&acc)[S::MB][S::NB]) {
+  int tm, tn;
+  nt_tile(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+  t0 = tm * S::BM;
+  v0 = g.v0 + tn * S::BN;
+  const NtOperand a{g.x + static_cast<size_t>(t0) * g.D, g.D, g.T - t0};
+  const NtOperand b{g.w + static_cast<size_t>(v0) * g.D, g.D, g.V - v0};
+  gemm_nt<S>(a, b, g.D, smem, acc);
+}
+
+template <class S>
+__global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_stats_kernel(LogitArgs g) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[S::kLds];
+  f32x16 acc[S::MB][S::NB];
+  int t0, v0;
+  logits_tile<S>(g, smem, t0, v0, acc);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wr = wave / S::WC, wc = wave % S::WC;
+  float2* red = reinterpret_cast<float2*>(smem);           // [WC][BM]
+  const int vw = v0 + 32 * S::NB * wc + 4 * (lane >> 5);   // the lane's first column
+  const bool edge = v0 + S::BN > g.V;
+#pragma unroll
+  for (int m = 0; m < S::MB; ++m) {
+    const int row = 32 * (S::MB * wr + m) + (lane & 31), t = t0 + row;
+    const int y = g.target[min(t, g.T - 1)];
+    const bool here = t < g.T && y >= v0 && y < v0 + S::BN && y < g.V;
+    float top = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < S::NB; ++n) {
+      asm volatile("" : "+a"(acc[m][n]));                  // one block's accumulators at a time
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int v = vw + 32 * n + 8 * (r >> 2) + (r & 3);
+        if (edge && v >= g.V) acc[m][n][r] = -INFINITY;
+        top = fmaxf(top, acc[m][n][r]);
+      }
+      if (here) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (vw + 32 * n + 8 * (r >> 2) + (r & 3) == y) g.zt[t] = acc[m][n][r];
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float from = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < S::NB; ++n)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sum += __expf(acc[m][n][r] - from);
+    sum += __shfl_xor(sum, 32);
+    if (lane < 32) red[wc * S::BM + row] = make_float2(top, sum);
+  }
+  __syncthreads();
+  for (int row = tid; row < S::BM; row += kNtThreads) {
+    if (t0 + row >= g.T) break;
+    float2 all = red[row];
+#pragma unroll
+    for (int c = 1; c < S::WC; ++c) {
+      const float2 o = red[c * S::BM + row];
+      const float top = fmaxf(all.x, o.x), from = top == -INFINITY ? 0.0f : top;
+      all = make_float2(top, all.y * __expf(all.x - from) + o.y * __expf(o.x - from));
+    }
+    g.part[static_cast<size_t>(t0 + row) * g.parts + (v0 - g.v0) / S::BN] = all;
+  }
+}
+
+// One wave a row joins the tiles' maxima and sums.
+__global__ __launch_bounds__(256) void head_join_kernel(const float2* part, int parts, const float* zt,
+                                                        const int32_t* target, int T, int V, float* loss, float* lse) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  const int y = target[t];
+  if (y < 0 || y >= V) {
+    if (lane == 0) loss[t] = lse[t] = 0.0f;
+    return;
+  }
+  const float2* p = part + static_cast<size_t>(t) * parts;
+  float top = -INFINITY;
+  for (int i = lane; i < parts; i += 64) top = fmaxf(top, p[i].x);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  const float from = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  for (int i = lane; i < parts; i += 64) sum += p[i].y * __expf(p[i].x - from);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+  if (lane == 0) {
+    const float l = logf(sum);
+    lse[t] = from + l;
+    loss[t] = (from - zt[t]) + l;                          // exact where the target is the largest
+  }
+}
+
+template <class S>
+__global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_probs_kernel(LogitArgs g) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[S::kLds];
+  f32x16 acc[S::MB][S::NB];
+  int t0, v0;
+  logits_tile<S>(g, smem, t0, v0, acc);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave / S::WC, wc = wave % S::WC;
+  const int tw = t0 + 32 * S::MB * wr, vw = v0 + 32 * S::NB * wc;   // the wave's first row and column
+  // P over z, in the accumulators
+#pragma unroll
+  for (int m = 0; m < S::MB; ++m) {
+    const int t = tw + 32 * m + (lane & 31), tc = min(t, g.T - 1);
+    const int y = g.target[tc];
+    const bool takes = t < g.T && y >= 0 && y < g.V;
+    const float lse = g.lse[tc], w = g.dloss[tc];
+#pragma unroll
+    for (int n = 0; n < S::NB; ++n) {
+      asm volatile("" : "+a"(acc[m][n]));
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int v = vw + 32 * n + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        float p = __expf(acc[m][n][r] - lse);
+        if (v == y) p -= 1.0f;
+        acc[m][n][r] = takes && v < g.V ? p * w : 0.0f;
+      }
+      asm volatile("" : "+a"(acc[m][n]));
+    }
+  }
+  constexpr int kTokB = 64 * S::MB;                        // bytes of the wave's rows, transposed
+  unsigned char* stg = smem + wave * (32 * S::NB * kTokB > 2048 * S::NB ? 32 * S::NB * kTokB : 2048 * S::NB);
+  static_assert(4 * (32 * S::NB * kTokB > 2048 * S::NB ? 32 * S::NB * kTokB : 2048 * S::NB) <= S::kLds, "LDS");
+  if (g.pt) {
+    // the transpose: columns as rows of 32 MB tokens
+#pragma unroll
+    for (int m = 0; m < S::MB; ++m)
+#pragma unroll
+      for (int n = 0; n < S::NB; ++n) {
+        asm volatile("" : "+a"(acc[m][n]));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int v = 32 * n + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+          *reinterpret_cast<bf16_t*>(stg + v * kTokB + 2 * (32 * m + (lane & 31))) = f32_to_bf16(acc[m][n][r]);
+        }
+      }
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    constexpr int kPieces = kTokB / 16;
+#pragma unroll 4
+    for (int i = 0; i < 32 * S::NB * kPieces / 64; ++i) {
+      const int at = 64 * i + lane, v = at / kPieces, c = at % kPieces;
+      const u32x4 d = *reinterpret_cast<const u32x4*>(stg + v * kTokB + 16 * c);
+      if (vw + v < g.v1 && tw + 8 * c < g.ldt)
+        *(gu32x4*)((gbyte*)(g.pt + static_cast<size_t>(vw - g.v0 + v) * g.ldt + tw + 8 * c)) = d;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  }
+  if (g.p)
+    store_rows<S>(g.p + static_cast<size_t>(tw) * g.ldp + (vw - g.v0), g.ldp, g.T - tw, g.ldp - (vw - g.v0), stg,
+                  [&](int m, int n, int r) { return acc[m][n][r]; });
+}
+
+struct ProductArgs {
+  const bf16_t* a;          // [M, lda]
+  const bf16_t* b;          // [N, ldb]
+  int M, N, K, lda, ldb;    // K a multiple of 64
+  int tiles_m, tiles_n, parts;
+  bf16_t* out;              // [M, N] bf16 (parts == 1), or ...
+  float* sums;              // ... [parts][M, N] fp32: part z of the reduction
+  int add;                  // added to what sums holds
+};
+
+template <class S>
+__global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_product_kernel(ProductArgs g) {
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[S::kLds];
+  const int tiles = g.tiles_m * g.tiles_n;
+  const int z = blockIdx.x / tiles;
+  int tm, tn;
+  nt_tile(blockIdx.x - z * tiles, g.tiles_m, g.tiles_n, tm, tn);
+  const int nk = g.K / kNtBK;
+  const int k0 = static_cast<int>(static_cast<int64_t>(nk) * z / g.parts), k1 = static_cast<int>(static_cast<int64_t>(nk) * (z + 1) / g.parts);
+  const int m0 = tm * S::BM, n0 = tn * S::BN;
+  f32x16 acc[S::MB][S::NB];
+  const NtOperand a{g.a + static_cast<size_t>(m0) * g.lda + k0 * kNtBK, g.lda, g.M - m0};
+  const NtOperand b{g.b + static_cast<size_t>(n0) * g.ldb + k0 * kNtBK, g.ldb, g.N - n0};
+  gemm_nt<S>(a, b, (k1 - k0) * kNtBK, smem, acc);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mw = m0 + 32 * S::MB * (wave / S::WC), nw = n0 + 32 * S::NB * (wave % S::WC);
+  if (g.sums == nullptr) {
+    store_rows<S>(g.out + static_cast<size_t>(mw) * g.N + nw, g.N, g.M - mw, g.N - nw, smem + wave * 2048 * S::NB,
+                  [&](int m, int n, int r) { return acc[m][n][r]; });
+    return;
+  }
+  float* sums = g.sums + static_cast<size_t>(z) * g.M * g.N;
+#pragma unroll
+  for (int m = 0; m < S::MB; ++m) {
+    const int row = mw + 32 * m + (lane & 31);
+#pragma unroll
+    for (int n = 0; n < S::NB; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = nw + 32 * n + 8 * q + 4 * (lane >> 5);
+        if (row >= g.M || col >= g.N) continue;
+        float4* at = reinterpret_cast<float4*>(sums + static_cast<size_t>(row) * g.N + col);
+        float4 v = make_float4(acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]);
+        if (g.add) {
+          const float4 o = *at;
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+        *at = v;
+      }
+  }
+}
+
+// dx from the parts of its sum, in their order
+__global__ __launch_bounds__(256) void head_round_kernel(const float* sums, int parts, int64_t n, bf16_t* out) {
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
+       i += static_cast<int64_t>(gridDim.x) * 1024) {
+    float4 v = *reinterpret_cast<const float4*>(sums + i);
+    for (int z = 1; z < parts; ++z) {
+      const float4 o = *reinterpret_cast<const float4*>(sums + z * n + i);
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
+}
+
+// dst [cols, ldd] = src [rows, cols]^T in 64 x 64 tiles; columns of dst from rows to
+// ldd (a multiple of 64) are zero, and so are those of rows whose target is outside
+// the vocabulary (what stands in them may be no number)
+__global__ __launch_bounds__(256) void head_transpose_kernel(const bf16_t* src, int rows, int cols, bf16_t* dst, int ldd,
+                                                             const int32_t* target, int V) {
+  __shared__ __attribute__((aligned(16))) bf16_t tile[64][72];
+  const int tid = threadIdx.x;
+  const int tr = ldd / 64;
+  const int r0 = static_cast<int>(blockIdx.x) % tr * 64, c0 = static_cast<int>(blockIdx.x) / tr * 64;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 32 * i + tid / 8, c = tid % 8 * 8;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    bool takes = r0 + r < rows && c0 + c < cols;
+    if (takes && target) {
+      const int y = target[r0 + r];
+      takes = y >= 0 && y < V;
+    }
+    if (takes) v = *reinterpret_cast<const u32x4*>(src + static_cast<size_t>(r0 + r) * cols + c0 + c);
+    *reinterpret_cast<u32x4*>(&tile[r][c]) = v;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = 32 * i + tid / 8, r = tid % 8 * 8;
+    if (c0 + c >= cols) continue;
+    union {
+      u32x4 v;
+      bf16_t e[8];
+    } o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o.e[j] = tile[r + j][c];
+    *reinterpret_cast<u32x4*>(dst + static_cast<size_t>(c0 + c) * ldd + r0 + r) = o.v;
+  }
+}
+
+__global__ __launch_bounds__(256) void head_zero_kernel(u32x4* out, int64_t n) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * 256)
+    out[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+constexpr int up(int n, int to) { return (n + to - 1) / to * to; }
+
+unsigned blocks_for(int64_t items) {
+  const int64_t want = (items + 255) / 256;
+  return static_cast<unsigned>(want < 4096 ? want : 4096);
+}
+
+// What a backward pass holds: P and its transpose for a piece of the vocabulary of
+// about 2^27 entries (268 MB each; whole tiles), W's piece transposed, x transposed,
+// dx's sums.  Larger pieces gain nothing, smaller ones lose in the tiles' last round.
+struct Plan {
+  int piece;                // columns of a piece, a multiple of 256
+  int ldt;                  // rows, rounded up to 64
+  int parts;                // parts of dx's reduction
+  bool sums;                // dx through fp32 sums
+  size_t p, pt, wt, xt, dx, bytes;
+};
+
+int row_tile(int rows) { return rows <= 32 ? 32 : (rows <= 64 ? 64 : (rows <= 128 ? 128 : 256)); }
+
+Plan plan(int rows, int cols, int vocab) {
+  Plan q{};
+  q.ldt = up(rows, 64);
+  int64_t piece = (int64_t{1} << 27) / q.ldt;
+  const int64_t by_w = (int64_t{1} << 27) / cols;
+  if (by_w < piece) piece = by_w;
+  piece = piece / 256 * 256;
+  if (piece < 2048) piece = 2048;
+  if (piece > up(vocab, 256)) piece = up(vocab, 256);
+  q.piece = static_cast<int>(piece);
+  const int tiles = (rows + row_tile(rows) - 1) / row_tile(rows) * ((cols + 255) / 256);
+  // enough workgroups for the CUs, with at least 16 stages each
+  int parts = (256 + tiles - 1) / tiles;
+  const int most = q.piece / (16 * kNtBK);
+  q.parts = parts < most ? parts : (most > 1 ? most : 1);
+  q.sums = q.parts > 1 || q.piece < vocab;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += (n + 255) / 256 * 256;
+    return here;
+  };
+  q.p = take(static_cast<size_t>(rows) * q.piece * 2);
+  q.pt = take(static_cast<size_t>(q.piece) * q.ldt * 2);
+  q.wt = take(static_cast<size_t>(cols) * q.piece * 2);
+  q.xt = take(static_cast<size_t>(cols) * q.ldt * 2);
+  q.dx = take(q.sums ? static_cast<size_t>(q.parts) * rows * cols * 4 : 0);
+  q.bytes = at;
+  return q;
+}
+
+template <class S>
+void launch_stats(LogitArgs g, hipStream_t st) {
+  g.tiles_m = (g.T + S::BM - 1) / S::BM;
+  g.tiles_n = (g.v1 - g.v0 + S::BN - 1) / S::BN;
+  head_stats_kernel<S><<<g.tiles_m * g.tiles_n, kNtThreads, 0, st>>>(g);
+}
+
+template <class S>
+void launch_probs(LogitArgs g, hipStream_t st) {
+  g.tiles_m = (g.T + S::BM - 1) / S::BM;
+  g.tiles_n = (g.v1 - g.v0 + S::BN - 1) / S::BN;
+  head_probs_kernel<S><<<g.tiles_m * g.tiles_n, kNtThreads, 0, st>>>(g);
+}
+
+template <class S>
+void launch_product(ProductArgs g, hipStream_t st) {
+  g.tiles_m = (g.M + S::BM - 1) / S::BM;
+  g.tiles_n = (g.N + S::BN - 1) / S::BN;
+  head_product_kernel<S><<<g.tiles_m * g.tiles_n * g.parts, kNtThreads, 0, st>>>(g);
+}
+
+}  // namespace
+
+size_t head_loss_workspace_bytes(int64_t rows, int cols, int vocab) {
+  const size_t parts = (vocab + 255) / 256;
+  const size_t forward = static_cast<size_t>(rows) * (parts * 8 + 4) + 512;
+  const size_t backward = plan(static_cast<int>(rows), cols, vocab).bytes;
+  const size_t n = forward > backward ? forward : backward;
+  return (n + 255) / 256 * 256;
+}
+
+hipError_t launch_head_loss_forward(int rows, int cols, int vocab, const bf16_t* x, const bf16_t* w,
+                                    const int32_t* target, float* loss, float* lse, void* workspace, hipStream_t st) {
+  LogitArgs g{};
+  g.x = x;
+  g.w = w;
+  g.target = target;
+  g.T = rows;
+  g.D = cols;
+  g.V = vocab;
+  g.v1 = vocab;
+  g.parts = (vocab + 255) / 256;
+  g.part = static_cast<float2*>(workspace);
+  g.zt = reinterpret_cast<float*>(g.part + static_cast<size_t>(rows) * g.parts);
+  switch (row_tile(rows)) {
+    case 32: launch_stats<Rows32>(g, st); break;
+    case 64: launch_stats<Rows64>(g, st); break;
+    case 128: launch_stats<Rows128>(g, st); break;
+    default: launch_stats<Wide>(g, st); break;
+  }
+  if (hipError_t e = hipGetLastError()) return e;
+  head_join_kernel<<<(rows + 3) / 4, 256, 0, st>>>(g.part, g.parts, g.zt, target, rows, vocab, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t* x, const bf16_t* w,
+                                     const int32_t* target, const float* lse, const float* dloss, bf16_t* dx,
+                                     bf16_t* dw, void* workspace, hipStream_t st) {
+  if (rows == 0) {
+    const int64_t n = static_cast<int64_t>(vocab) * cols / 8;
+    if (dw) head_zero_kernel<<<blocks_for(n), 256, 0, st>>>(reinterpret_cast<u32x4*>(dw), n);
+    return hipGetLastError();
+  }
+  const Plan q = plan(rows, cols, vocab);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  bf16_t* p = reinterpret_cast<bf16_t*>(ws + q.p);
+  bf16_t* pt = reinterpret_cast<bf16_t*>(ws + q.pt);
+  bf16_t* wt = reinterpret_cast<bf16_t*>(ws + q.wt);
+  bf16_t* xt = reinterpret_cast<bf16_t*>(ws + q.xt);
+  float* sums = reinterpret_cast<float*>(ws + q.dx);
+  const int col_tiles = (cols + 63) / 64;
+  if (dw) head_transpose_kernel<<<col_tiles * (q.ldt / 64), 256, 0, st>>>(x, rows, cols, xt, q.ldt, target, vocab);
+  for (int v0 = 0; v0 < vocab; v0 += q.piece) {
+    const int v1 = vocab - v0 < q.piece ? vocab : v0 + q.piece;
+    const int ldp = up(v1 - v0, 64);
+    LogitArgs g{};
+    g.x = x;
+    g.w = w;
+    g.target = target;
+    g.T = rows;
+    g.D = cols;
+    g.V = vocab;
+    g.v0 = v0;
+    g.v1 = v1;
+    g.lse = lse;
+    g.dloss = dloss;
+    g.p = dx ? p : nullptr;
+    g.pt = dw ? pt : nullptr;
+    g.ldp = ldp;
+    g.ldt = q.ldt;
+    switch (row_tile(rows)) {                              // (all ldt columns of the transpose are written)
+      case 32:
+      case 64: launch_probs<Rows64>(g, st); break;
+      case 128: launch_probs<Rows128>(g, st); break;
+      default: launch_probs<Wide>(g, st); break;
+    }
+    if (dw) {
+      ProductArgs d{};
+      d.a = pt;
+      d.b = xt;
+      d.M = v1 - v0;
+      d.N = cols;
+      d.K = q.ldt;
+      d.lda = d.ldb = q.ldt;
+      d.parts = 1;
+      d.out = dw + static_cast<size_t>(v0) * cols;
+      launch_product<Wide>(d, st);
+    }
+    if (dx) {
+      head_transpose_kernel<<<col_tiles * (ldp / 64), 256, 0, st>>>(w + static_cast<size_t>(v0) * cols, v1 - v0, cols,
+                                                                    wt, ldp, nullptr, 0);
+      ProductArgs d{};
+      d.a = p;
+      d.b = wt;
+      d.M = rows;
+      d.N = cols;
+      d.K = ldp;
+      d.lda = d.ldb = ldp;
+      const int most = ldp / kNtBK;
+      d.parts = q.parts < most ? q.parts : most;
+      d.out = dx;
+      d.sums = q.sums ? sums : nullptr;
+      d.add = v0 > 0;
+      switch (row_tile(rows)) {
+        case 32: launch_product<Rows32>(d, st); break;
+        case 64: launch_product<Rows64>(d, st); break;
+        case 128: launch_product<Rows128>(d, st); break;
+        default: launch_product<Wide>(d, st); break;
+      }
+    }
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  if (dx && q.sums) {
+    const int64_t n = static_cast<int64_t>(rows) * cols;
+    head_round_kernel<<<blocks_for(n / 4), 256, 0, st>>>(sums, q.parts, n, dx);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe
