@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "grouped_gemm.h"
+#include "mma_stream.h"
 
 namespace moe {
 namespace {
@@ -87,7 +88,7 @@ __device__ __forceinline__ u32x4 load16(const void* base, uint32_t off) {
 // 16- and 2-byte pieces of many lines: 87 us against 75 for 32 tokens' gate/up at
 // D = 4096, F = 1024).  No barrier before the waves' parts meet.
 template <int MODE, int TM, int G>
-__global__ __launch_bounds__(256, TM == 1 ? 3 : (TM == 2 ? 2 : 1)) void int4_rows_kernel(Int4Args a) {
+__global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Args a) {
   constexpr int NB = 4;                                   // 16-row weight blocks of a wave
   constexpr int kCols = MODE == kInt4GateUp ? 32 : 64;    // output columns of a wave
   constexpr int GC = kColBlock / G;                       // groups of a packed block
@@ -369,10 +370,239 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : (TM == 2 ? 2 : 1)) void int4_row
   };
   // with as few row loads as hold the chunk
   const int left = M - m0;
-  if (TM > 2 && left > 32) chunk(std::integral_constant<int, 4 * TM>{});
-  else if (TM > 1 && left > 16) chunk(std::integral_constant<int, (TM > 1 ? 8 : 4)>{});
+  if (TM > 1 && left > 16) chunk(std::integral_constant<int, 4 * TM>{});
   else if (left > 4) chunk(std::integral_constant<int, 4>{});
   else chunk(std::integral_constant<int, 1>{});
+}
+
+// Many rows an expert: one workgroup computes 128 rows x 256 weight rows (gate_up:
+// 128 gate rows and the up rows of the same columns) over the whole reduction, a
+// wave 64 of the weight rows (as above) and all 128 rows.  The rows' columns come
+// 128 at a time by direct global->LDS loads into two buffers, whole lines, the
+// 16-byte pieces of row r XOR-swizzled by r mod 16; weights go straight into
+// registers two stages ahead and are widened once for the 8 token blocks.  At most
+// 64 columns are summed before the scales: 32 operand registers a wave, so that two
+// workgroups share a CU and one's conversions run beside the other's MFMAs.
+// Tiles in order of expert, column tile, row block, each XCD a run of them, so that
+// an expert's rows and a column tile's weights stay behind one L2.
+template <int MODE, int G>
+__global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
+  constexpr int NB = 4, TB = 8, kRows = 16 * TB;
+  constexpr int kCols = MODE == kInt4GateUp ? 32 : 64;    // output columns of a wave
+  constexpr int GC = kColBlock / G;                       // scales of a row and block
+  constexpr int kStage = kRows * kColBlock * 2;           // 32 KB
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // ---- whose tile (the shared expert's first); lane l counts experts 4 l .. 4 l + 3
+  const int chunks_s = a.tiles_s > 0 ? (a.T + kRows - 1) / kRows : 0;
+  int off[5];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) off[j] = a.offsets[min(4 * lane + j, a.E)];
+  int sum = 0;
+#pragma unroll
+  for (int j = 0; j < 5; ++j) {
+    off[j] = min(max(off[j], j ? off[j - 1] : 0), a.S);
+    if (j) sum += (off[j] - off[j - 1] + kRows - 1) / kRows;
+  }
+  int end = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(end, d);
+    if (lane >= d) end += v;
+  }
+  const int n_s = chunks_s * a.tiles_s;
+  const int total = n_s + __builtin_amdgcn_readlane(end, 63) * a.tiles_r;
+  const int xcd = blockIdx.x % kGemmXcds, in_xcd = blockIdx.x / kGemmXcds;
+  const int share = total / kGemmXcds, rem = total % kGemmXcds;
+  if (in_xcd >= share + (xcd < rem ? 1 : 0)) return;
+  int t = xcd * share + min(xcd, rem) + in_xcd;
+  const bool shared = t < n_s;
+  int e = 0, lo = 0, M = a.T, tile, m0;
+  if (shared) {
+    m0 = t % chunks_s * kRows;
+    tile = t / chunks_s;
+  } else {
+    t -= n_s;
+    const int slot = t / a.tiles_r;
+    const int src = __ffsll(static_cast<unsigned long long>(__ballot(slot < end))) - 1;
+    int first = end - sum, j = 0;                         // chunks before expert 4 l + j
+#pragma unroll
+    for (int q = 1; q < 4; ++q) {
+      const int n = (off[q] - off[q - 1] + kRows - 1) / kRows;
+      if (j == q - 1 && slot >= first + n) {
+        first += n;
+        j = q;
+      }
+    }
+    const int from = j == 0 ? off[0] : (j == 1 ? off[1] : (j == 2 ? off[2] : off[3]));
+    const int to = j == 0 ? off[1] : (j == 1 ? off[2] : (j == 2 ? off[3] : off[4]));
+    e = min(__builtin_amdgcn_readlane(4 * lane + j, src), a.E - 1);
+    lo = __builtin_amdgcn_readlane(from, src);
+    M = __builtin_amdgcn_readlane(to, src) - lo;
+    const int local = t - __builtin_amdgcn_readlane(first, src) * a.tiles_r;
+    const int chunks = (M + kRows - 1) / kRows;
+    m0 = local % chunks * kRows;
+    tile = local / chunks;
+  }
+  const int K = shared ? a.Ks : a.K;
+  const int N = shared ? a.Ns : a.N;
+  const int Nw = MODE == kInt4GateUp ? 2 * N : N;
+  const int ncb = K / kColBlock;
+  const int n0 = (tile * 4 + wave) * kCols;
+  const int valid = min(kRows, M - m0);
+  const int tbv = (valid + 15) / 16;                      // token blocks with rows
+
+  // ---- sources
+  const uint8_t* wmat = shared ? a.w_shared : a.w_routed + static_cast<size_t>(e) * Nw * (K / 2);
+  const bf16_t* smat = shared ? a.s_shared : a.s_routed + static_cast<size_t>(e) * Nw * (K / G);
+  auto first_row = [&](int b) {
+    return MODE == kInt4GateUp ? (b < 2 ? n0 + 16 * b : N + n0 + 16 * (b - 2)) : n0 + 16 * b;
+  };
+  const uint8_t* wb[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) wb[b] = wmat + static_cast<size_t>(first_row(b) / kRowBlock) * ncb * kBlockBytes;
+  // lane l loads the scales of row l of the wave's 64
+  const bf16_t* sp = smat + static_cast<size_t>(first_row(lane >> 4) + (lane & 15)) * (K / G);
+  // load q of a wave: rows 4 (8 wave + q) + lane / 16, slot lane mod 16
+  const unsigned char* xbase = reinterpret_cast<const unsigned char*>(
+      shared ? a.a_shared + static_cast<size_t>(m0) * K
+             : (a.gather ? a.a_routed : a.a_routed + static_cast<size_t>(lo + m0) * K));
+  uint32_t xo[TB];
+#pragma unroll
+  for (int q = 0; q < TB; ++q) {
+    const int r = 4 * (TB * wave + q) + (lane >> 4);
+    int row = min(r, valid - 1);
+    if (!shared && a.gather) row = min(max(a.gather[lo + m0 + row], 0), a.T - 1);
+    xo[q] = (static_cast<uint32_t>(row) * static_cast<uint32_t>(K) + 8u * ((lane & 15) ^ (r & 15))) * 2u;
+  }
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+  auto issue_rows = [&](int cb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < TB; ++q)
+      dma16_off(xbase + static_cast<size_t>(cb) * (kColBlock * 2), xo[q],
+                lds0 + static_cast<uint32_t>(cb & 1) * kStage + (TB * wave + q) * 1024u);
+  };
+  struct Stage {
+    u32x4 w[NB];
+    uint32_t s[(GC + 1) / 2];                             // GC scales, two a word (GC 1: one)
+  };
+  auto load = [&](Stage& f, int cb) __attribute__((always_inline)) {
+    const bool in = cb < ncb;                             // (past the end every lane reads the same)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      f.w[b] = load16<false>(wb[b] + static_cast<size_t>(in ? cb : 0) * kBlockBytes, in ? lane * 16u : 0u);
+    const bf16_t* from = sp + (in ? cb : 0) * GC;
+    if constexpr (GC == 1) {
+      f.s[0] = *from;
+    } else {
+#pragma unroll
+      for (int g = 0; g < GC / 2; ++g) f.s[g] = reinterpret_cast<const uint32_t*>(from)[g];
+    }
+  };
+  const Widen widen;
+  f32x4 acc[TB][NB];
+#pragma unroll
+  for (int i = 0; i < TB; ++i)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[i][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // a stage over the row block's NT live token blocks
+  auto compute = [&](Stage& f, int cb, auto nt_tag) __attribute__((always_inline)) {
+    constexpr int NT = decltype(nt_tag)::value;
+    const unsigned char* X = smem + (cb & 1) * kStage;
+    const u32x4 offset = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};   // -136
+    constexpr int SG = G == 32 ? 1 : 2;                   // MFMA steps before the scales
+#pragma unroll
+    for (int part = 0; part < 4 / SG; ++part) {
+      const int g = part * SG * 32 / G;                   // the group
+      const uint32_t word = f.s[g / 2];
+      const uint32_t own = GC == 1 || g % 2 == 0 ? word << 16 : word & 0xffff0000u;
+      const auto p = __builtin_amdgcn_permlane32_swap(own, own, false, false);
+      const auto p01 = __builtin_amdgcn_permlane16_swap(p[0], p[0], false, false);
+      const auto p23 = __builtin_amdgcn_permlane16_swap(p[1], p[1], false, false);
+      const float sc[NB] = {__uint_as_float(p01[0]), __uint_as_float(p01[1]), __uint_as_float(p23[0]),
+                            __uint_as_float(p23[1])};
+      bf16x8 w[SG][NB];
+#pragma unroll
+      for (int i = 0; i < SG; ++i)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) w[i][b] = widen(f.w[b][part * SG + i]);
+      // (the registers of the packed weights are free: the next stage's)
+      if (part == 4 / SG - 1) load(f, cb + 1);
+      auto read = [&](bf16x8 (&x)[SG], int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < SG; ++k)
+          x[k] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
+                                                X + (16 * i + (lane & 15)) * 256 +
+                                                (((4 * (part * SG + k) + (lane >> 4)) ^ (lane & 15)) << 4)));
+      };
+      bf16x8 x[2][SG];
+      read(x[0], 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if (i + 1 < NT) read(x[(i + 1) & 1], i + 1);
+        f32x4 start = {0.f, 0.f, 0.f, 0.f}, y[NB];
+#pragma unroll
+        for (int k = 0; k < SG; ++k)
+          start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][k], __builtin_bit_cast(bf16x8, offset), start, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < SG; ++k)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            y[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][k], w[k][b], k == 0 ? start : y[b], 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][b][r] = fmaf(sc[b], y[b][r], acc[i][b][r]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+
+  // stage cb: its rows were issued a stage before, its weights half a stage
+  Stage f;
+  issue_rows(0);
+  load(f, 0);
+  auto k_loop = [&](auto nt_tag) __attribute__((always_inline)) {
+    for (int cb = 0; cb < ncb; ++cb) {
+      __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (cb + 1 < ncb) issue_rows(cb + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(f, cb, nt_tag);
+    }
+  };
+  if (tbv > 6) k_loop(std::integral_constant<int, 8>{});
+  else if (tbv > 4) k_loop(std::integral_constant<int, 6>{});
+  else if (tbv > 2) k_loop(std::integral_constant<int, 4>{});
+  else k_loop(std::integral_constant<int, 2>{});
+
+  // ---- out through LDS: [row][the tile's columns], pieces of 16 bytes swizzled
+  constexpr int kTileCols = 4 * kCols, kPieces = kTileCols / 8;
+  __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+  __syncthreads();
+  auto piece_at = [&](int row, int piece) { return smem + row * (kTileCols * 2) + ((piece ^ (((row >> 2) & 3) << 1)) << 4); };
+#pragma unroll
+  for (int i = 0; i < TB; ++i)
+#pragma unroll
+    for (int b = 0; b < kCols / 16; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v = acc[i][b][r];
+        if constexpr (MODE == kInt4GateUp) v = v * __builtin_amdgcn_rcpf(1.0f + __expf(-v)) * acc[i][(b + 2) % NB][r];
+        const int row = 16 * i + 4 * (lane >> 4) + r, col = kCols * wave + 16 * b + (lane & 15);
+        *reinterpret_cast<bf16_t*>(piece_at(row, col >> 3) + 2 * (col & 7)) = f32_to_bf16(v);
+      }
+  __syncthreads();
+  bf16_t* out = (shared ? a.out_shared : a.out_routed + static_cast<size_t>(lo) * N) + static_cast<size_t>(m0) * N + tile * kTileCols;
+  for (int i = tid; i < valid * kPieces; i += 256) {
+    const int row = i / kPieces, piece = i % kPieces;
+    *reinterpret_cast<u32x4*>(out + static_cast<size_t>(row) * N + 8 * piece) =
+        *reinterpret_cast<const u32x4*>(piece_at(row, piece));
+  }
 }
 
 // ------------------------------------------------------------------ load time
@@ -480,9 +710,26 @@ hipError_t launch_rows(Int4Args a, int group, hipStream_t st) {
 }
 
 template <int MODE>
+hipError_t launch_tiles4(Int4Args a, int group, hipStream_t st) {
+  constexpr int kRows = 128, kTileCols = MODE == kInt4GateUp ? 128 : 256;
+  a.tiles_r = a.N / kTileCols;
+  a.tiles_s = a.Ns / kTileCols;
+  const int64_t most = static_cast<int64_t>(a.E) + a.S / kRows;
+  const int64_t tiles = (a.S < most ? a.S : most) * a.tiles_r + static_cast<int64_t>((a.T + kRows - 1) / kRows) * a.tiles_s;
+  const int64_t grid = (tiles + kGemmXcds - 1) / kGemmXcds * kGemmXcds;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  switch (group) {
+    case 32: int4_tile_kernel<MODE, 32><<<static_cast<unsigned>(grid), 256, 0, st>>>(a); break;
+    case 64: int4_tile_kernel<MODE, 64><<<static_cast<unsigned>(grid), 256, 0, st>>>(a); break;
+    default: int4_tile_kernel<MODE, 128><<<static_cast<unsigned>(grid), 256, 0, st>>>(a); break;
+  }
+  return hipGetLastError();
+}
+
+template <int MODE>
 hipError_t launch_int4(const Int4Args& a, int group, hipStream_t st) {
   const int mean = a.S / a.E;
-  if (mean >= 32) return launch_rows<MODE, 4>(a, group, st);
+  if (mean >= 48) return launch_tiles4<MODE>(a, group, st);
   if (mean >= 12) return launch_rows<MODE, 2>(a, group, st);
   return launch_rows<MODE, 1>(a, group, st);
 }
