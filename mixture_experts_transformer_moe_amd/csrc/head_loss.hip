@@ -27,12 +27,23 @@ namespace {
 typedef __attribute__((address_space(1))) unsigned char gbyte;
 typedef __attribute__((address_space(1))) u32x4 gu32x4;
 
-// row blocks by the rows of the batch: 256 x 256 tiles, and narrower ones that
-// leave small batches bound by the weights
-using Wide = NtShape<2, 2, 4, 4>;
-using Rows128 = NtShape<1, 4, 4, 2>;
-using Rows64 = NtShape<1, 4, 2, 2>;
+// Tiles: 256 x 256 with one workgroup a CU, 128 x 128 with two, and low ones that
+// leave small batches bound by the weights.
+enum Tile { kRows32, kRows64, kMid, kWide };
 using Rows32 = NtShape<1, 4, 1, 2>;
+using Rows64 = NtShape<1, 4, 2, 2>;
+using Mid = NtShape<2, 2, 2, 2>;
+using Wide = NtShape<2, 2, 4, 4>;
+
+template <class F>
+void with_tile(Tile t, F&& f) {
+  switch (t) {
+    case kRows32: f(Rows32{}); break;
+    case kRows64: f(Rows64{}); break;
+    case kMid: f(Mid{}); break;
+    default: f(Wide{}); break;
+  }
+}
 
 // The bf16 tile of a wave (32 MB rows, 32 NB columns; value(m, n, r) gives register
 // r of block (m, n), rounded) through its LDS, stored as whole row segments: rows
@@ -363,33 +374,83 @@ unsigned blocks_for(int64_t items) {
 }
 
 // What a backward pass holds: P and its transpose for a piece of the vocabulary of
-// about 2^27 entries (268 MB each; whole tiles), W's piece transposed, x transposed,
-// dx's sums.  Larger pieces gain nothing, smaller ones lose in the tiles' last round.
+// about 2^27 entries (268 MB each; whole tiles; at least 8192 columns, under which
+// dx's fp32 sums, read and written once a piece, would cost a third of its product),
+// W's piece transposed, x transposed, dx's sums.
 struct Plan {
   int piece;                // columns of a piece, a multiple of 256
   int ldt;                  // rows, rounded up to 64
-  int parts;                // parts of dx's reduction
+  Tile tile;                // of dx's product
+  int parts;                // parts of its reduction
   bool sums;                // dx through fp32 sums
   size_t p, pt, wt, xt, dx, bytes;
 };
 
-int row_tile(int rows) { return rows <= 32 ? 32 : (rows <= 64 ? 64 : (rows <= 128 ? 128 : 256)); }
+int rows_of(Tile t) { return t == kRows32 ? 32 : (t == kRows64 ? 64 : (t == kMid ? 128 : 256)); }
+int cols_of(Tile t) { return t == kMid ? 128 : 256; }
+
+int64_t tiles_of(Tile t, int64_t M, int64_t N) {
+  return (M + rows_of(t) - 1) / rows_of(t) * ((N + cols_of(t) - 1) / cols_of(t));
+}
+
+// Time of n tiles over K in us: rounds of what the CUs hold at once (two of 128 x 128
+// a CU; a last round that leaves one a CU runs its tiles faster), each a start and an
+// end and K's stages.  Measured on 8192 rows by 32768 columns: 540, 898, 1672 us at K
+// = 1024, 2048, 4096 in 256 x 256 tiles (16 rounds), 550, 990, 2016 in 128 x 128
+// (32 rounds).  At 384 x 100352 over 4096 the narrow tiles' finer rounds win (340 us
+// against 397), at 1024 rows they lose (820 against 715).
+double cost(Tile t, int64_t n, int64_t K) {
+  if (t == kWide) return static_cast<double>((n + 255) / 256) * (7.4 + 0.0236 * K);
+  const int64_t left = n % 512;
+  return (n / 512 + (left == 0 ? 0.0 : (left <= 256 ? 0.65 : 1.0))) * (1.5 + 0.0150 * K);
+}
+
+// The tile for an M x N product over K: low ones where the batch is that small
+// (bound by the reads of the other operand), else the cheaper of the two others.
+Tile pick(int64_t M, int64_t N, int64_t K, int lowest = 32) {
+  if (M <= 32 && lowest <= 32) return kRows32;
+  if (M <= 64) return kRows64;
+  return cost(kMid, tiles_of(kMid, M, N), K) < cost(kWide, tiles_of(kWide, M, N), K) ? kMid : kWide;
+}
+
+// dx's product: its tile, and the parts of its reduction that fill the CUs
+struct Split {
+  Tile tile;
+  int parts;
+};
+
+Split pick_split(int64_t M, int64_t N, int64_t K) {
+  Split best{kWide, 1};
+  double least = -1.0;
+  for (Tile t : {kRows32, kRows64, kMid, kWide}) {
+    if ((t == kRows32 && M > 32) || (t == kRows64 && M > 64)) continue;
+    const int64_t tiles = tiles_of(t, M, N), most = K / (16 * kNtBK);    // at least 16 stages each
+    int64_t parts = (t == kWide ? 256 : 512) / tiles;
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+    // with what the parts write and the last kernel reads, at 4.9 TB/s
+    const double c = cost(t, tiles * parts, K / parts) + static_cast<double>(parts) * M * N * 8 / 4.9e6;
+    if (least < 0 || c < least) {
+      least = c;
+      best = Split{t, static_cast<int>(parts)};
+    }
+  }
+  return best;
+}
 
 Plan plan(int rows, int cols, int vocab) {
   Plan q{};
   q.ldt = up(rows, 64);
-  int64_t piece = (int64_t{1} << 27) / q.ldt;
-  const int64_t by_w = (int64_t{1} << 27) / cols;
+  auto most = [](int64_t least, int64_t entries) { return entries > least ? entries : least; };
+  int64_t piece = most(8192, (int64_t{1} << 27) / q.ldt);
+  const int64_t by_w = most(2048, (int64_t{1} << 27) / cols);
   if (by_w < piece) piece = by_w;
   piece = piece / 256 * 256;
-  if (piece < 2048) piece = 2048;
   if (piece > up(vocab, 256)) piece = up(vocab, 256);
   q.piece = static_cast<int>(piece);
-  const int tiles = (rows + row_tile(rows) - 1) / row_tile(rows) * ((cols + 255) / 256);
-  // enough workgroups for the CUs, with at least 16 stages each
-  int parts = (256 + tiles - 1) / tiles;
-  const int most = q.piece / (16 * kNtBK);
-  q.parts = parts < most ? parts : (most > 1 ? most : 1);
+  const Split split = pick_split(rows, cols, q.piece);
+  q.tile = split.tile;
+  q.parts = split.parts;
   q.sums = q.parts > 1 || q.piece < vocab;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -408,6 +469,7 @@ Plan plan(int rows, int cols, int vocab) {
 
 template <class S>
 void launch_stats(LogitArgs g, hipStream_t st) {
+  g.parts = (g.V + S::BN - 1) / S::BN;
   g.tiles_m = (g.T + S::BM - 1) / S::BM;
   g.tiles_n = (g.v1 - g.v0 + S::BN - 1) / S::BN;
   head_stats_kernel<S><<<g.tiles_m * g.tiles_n, kNtThreads, 0, st>>>(g);
@@ -430,7 +492,7 @@ void launch_product(ProductArgs g, hipStream_t st) {
 }  // namespace
 
 size_t head_loss_workspace_bytes(int64_t rows, int cols, int vocab) {
-  const size_t parts = (vocab + 255) / 256;
+  const size_t parts = (vocab + 127) / 128;                 // (of the narrowest tile)
   const size_t forward = static_cast<size_t>(rows) * (parts * 8 + 4) + 512;
   const size_t backward = plan(static_cast<int>(rows), cols, vocab).bytes;
   const size_t n = forward > backward ? forward : backward;
@@ -447,15 +509,11 @@ hipError_t launch_head_loss_forward(int rows, int cols, int vocab, const bf16_t*
   g.D = cols;
   g.V = vocab;
   g.v1 = vocab;
-  g.parts = (vocab + 255) / 256;
+  const Tile t = pick(rows, vocab, cols);
+  g.parts = (vocab + cols_of(t) - 1) / cols_of(t);
   g.part = static_cast<float2*>(workspace);
   g.zt = reinterpret_cast<float*>(g.part + static_cast<size_t>(rows) * g.parts);
-  switch (row_tile(rows)) {
-    case 32: launch_stats<Rows32>(g, st); break;
-    case 64: launch_stats<Rows64>(g, st); break;
-    case 128: launch_stats<Rows128>(g, st); break;
-    default: launch_stats<Wide>(g, st); break;
-  }
+  with_tile(t, [&](auto s) { launch_stats<decltype(s)>(g, st); });
   if (hipError_t e = hipGetLastError()) return e;
   head_join_kernel<<<(rows + 3) / 4, 256, 0, st>>>(g.part, g.parts, g.zt, target, rows, vocab, loss, lse);
   return hipGetLastError();
@@ -496,12 +554,8 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
     g.pt = dw ? pt : nullptr;
     g.ldp = ldp;
     g.ldt = q.ldt;
-    switch (row_tile(rows)) {                              // (all ldt columns of the transpose are written)
-      case 32:
-      case 64: launch_probs<Rows64>(g, st); break;
-      case 128: launch_probs<Rows128>(g, st); break;
-      default: launch_probs<Wide>(g, st); break;
-    }
+    // (64 rows at least: all ldt columns of the transpose have to be written)
+    with_tile(pick(rows, v1 - v0, cols, 64), [&](auto s) { launch_probs<decltype(s)>(g, st); });
     if (dw) {
       ProductArgs d{};
       d.a = pt;
@@ -512,7 +566,7 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
       d.lda = d.ldb = q.ldt;
       d.parts = 1;
       d.out = dw + static_cast<size_t>(v0) * cols;
-      launch_product<Wide>(d, st);
+      with_tile(pick(d.M, d.N, d.K), [&](auto s) { launch_product<decltype(s)>(d, st); });
     }
     if (dx) {
       head_transpose_kernel<<<col_tiles * (ldp / 64), 256, 0, st>>>(w + static_cast<size_t>(v0) * cols, v1 - v0, cols,
@@ -529,12 +583,7 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
       d.out = dx;
       d.sums = q.sums ? sums : nullptr;
       d.add = v0 > 0;
-      switch (row_tile(rows)) {
-        case 32: launch_product<Rows32>(d, st); break;
-        case 64: launch_product<Rows64>(d, st); break;
-        case 128: launch_product<Rows128>(d, st); break;
-        default: launch_product<Wide>(d, st); break;
-      }
+      with_tile(q.tile, [&](auto s) { launch_product<decltype(s)>(d, st); });
     }
     if (hipError_t e = hipGetLastError()) return e;
   }
