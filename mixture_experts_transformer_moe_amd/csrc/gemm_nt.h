@@ -14,6 +14,13 @@
 //     next stage has landed: it was issued three steps before.
 //   * Rows past the last are the last row again (their results are not stored).
 //     K is a multiple of 8; pieces past its end read zeros.
+//   * BT: B lies the other way, the reduction along its columns' rows (B [K, N], N
+//     a multiple of 8).  A stage is then 64 of its rows, 16-byte units of row r
+//     XOR-swizzled by 4 (r mod 4), and gfx950's transposing LDS read hands a lane 4
+//     consecutive rows of one column, two reads an operand: in a group of 16 lanes
+//     it returns to lane 4a + b element b of the 8-byte pieces addressed by lanes a,
+//     a + 4, a + 8 and a + 12.  Rows past the reduction's end are its last one again:
+//     A has to hold zeros there.
 #pragma once
 
 #include <type_traits>
@@ -39,10 +46,19 @@ struct NtShape {
 };
 
 struct NtOperand {
-  const bf16_t* p;     // the tile's first row
+  const bf16_t* p;     // the tile's first row (BT: its first column in row 0)
   int ld;              // elements between rows, a multiple of 8
-  int rows;            // rows from p on that exist (>= 1)
+  int rows;            // rows from p on that exist (>= 1; BT: columns, a multiple of 8)
+  int depth;           // BT: rows of the reduction that exist (>= 1)
 };
+
+typedef short nt_v4i16 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint2 nt_read_tr(uint32_t at) {
+  typedef __attribute__((address_space(3))) nt_v4i16 lds_v4;
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (lds_v4*)(reinterpret_cast<__attribute__((address_space(3))) bf16_t*>(at))));
+}
 
 // a pointer that is the same in every lane, made visibly so
 template <typename T>
@@ -71,7 +87,7 @@ __device__ __forceinline__ void nt_each(F&& f, std::integer_sequence<int, Q...>)
   (f(std::integral_constant<int, Q>{}), ...);
 }
 
-template <class S>
+template <class S, bool BT = false>
 __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, int K, unsigned char* smem,
                                         f32x16 (&acc)[S::MB][S::NB]) {
   constexpr int MB = S::MB, NB = S::NB;
@@ -84,10 +100,19 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
   const bool ragged = K % kNtBK != 0;
 
   // load q of a wave: rows 8 (NA wave + q) .. + 7 of A's tile, then the same of B's
+  // (BT: the stage's rows, 512 / BN of them a load)
+  constexpr int kBU = S::BN / 8;                             // BT: 16-byte units of a row
+  constexpr int kBR = 64 / kBU;                              // BT: rows of a load
+  auto bt_row = [&](int q) { return kBR * (NBL * wave + q - NA) + lane / kBU; };
+  auto bt_col = [&](int q) { return min(8 * ((lane % kBU) ^ (4 * (bt_row(q) & 3))), b.rows - 8); };
   uint32_t off[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     const bool of_a = q < NA;
+    if (BT && !of_a) {
+      off[q] = (static_cast<uint32_t>(bt_row(q)) * static_cast<uint32_t>(b.ld) + static_cast<uint32_t>(bt_col(q))) * 2u;
+      continue;
+    }
     const int row = 8 * (of_a ? NA * wave + q : NBL * wave + q - NA) + (lane >> 3);
     const int piece = (lane & 7) ^ nt_swizzle(row);
     const int r = min(row, (of_a ? a.rows : b.rows) - 1);
@@ -100,10 +125,15 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
   auto issue = [&](int kb, int buf, auto q_tag, bool last) __attribute__((always_inline)) {
     constexpr int q = decltype(q_tag)::value;
     constexpr bool of_a = q < NA;
-    const unsigned char* base = (of_a ? pa : pb) + static_cast<size_t>(kb) * (kNtBK * 2);
+    const size_t step = BT && !of_a ? static_cast<size_t>(b.ld) * (kNtBK * 2) : kNtBK * 2;
+    const unsigned char* base = (of_a ? pa : pb) + kb * step;
     const uint32_t at = lds0 + static_cast<uint32_t>(buf) * S::kStage +
                         (of_a ? NA * 1024u * wave : S::BM * 128u + NBL * 1024u * wave);
-    if (last && ragged) {
+    if (BT && !of_a && last) {
+      const int row = min(bt_row(q), b.depth - 1 - kb * kNtBK);
+      const uint32_t o = (static_cast<uint32_t>(row) * static_cast<uint32_t>(b.ld) + static_cast<uint32_t>(bt_col(q))) * 2u;
+      nt_dma<(q - NA) * 1024>(base, o, __builtin_amdgcn_readfirstlane(at));
+    } else if (last && ragged) {
       // the last stage of a ragged reduction: pieces past its end are zeros
       const int row = 8 * (of_a ? NA * wave + q : NBL * wave + q - NA) + (lane >> 3);
       const int col = kb * kNtBK + 8 * ((lane & 7) ^ nt_swizzle(row));
@@ -130,9 +160,23 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
   struct Frag {
     u32x4 a[MB], b[NB];
   };
+  // BT: the lane's piece of row (lane / 16 / 2) 8 + (lane mod 16) / 4 of a step
+  uint32_t tr_off[NB];
+  if constexpr (BT) {
+    const int grp = lane >> 4, j = lane & 15;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+      tr_off[n] = static_cast<uint32_t>((8 * (grp >> 1) + (j >> 2)) * (kBU * 16) +
+                                        (((4 * (NB * wc + n) + 2 * (grp & 1) + ((j & 3) >> 1)) ^ (4 * (j >> 2))) << 4) +
+                                        8 * (j & 1));
+  }
   auto read_one = [&](Frag& f, int buf, int s, int i) __attribute__((always_inline)) {
     const unsigned char* base = smem + buf * S::kStage;
-    if (i < NB) f.b[i] = *reinterpret_cast<const u32x4*>(base + S::BM * 128 + (NB * wc + i) * 4096 + piece_off[s]);
+    if (BT && i < NB) {
+      const uint32_t at = lds0 + static_cast<uint32_t>(buf) * S::kStage + S::BM * 128u + 16u * s * (kBU * 16) + tr_off[i];
+      const uint2 lo = nt_read_tr(at), hi = nt_read_tr(at + 4 * (kBU * 16));
+      f.b[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
+    } else if (i < NB) f.b[i] = *reinterpret_cast<const u32x4*>(base + S::BM * 128 + (NB * wc + i) * 4096 + piece_off[s]);
     else f.a[i - NB] = *reinterpret_cast<const u32x4*>(base + (MB * wr + i - NB) * 4096 + piece_off[s]);
   };
   auto mfma = [&](const Frag& f, auto&& op) __attribute__((always_inline)) {

@@ -11,9 +11,9 @@
 // the tile's columns go out (8 bytes for 256 columns) and a second kernel joins
 // them in a fixed order.  Backward: the vocabulary goes by in pieces; per piece z
 // is computed again, P leaves the accumulators once as bf16, row-major both ways
-// (P for dx, its transpose for dW), and two products follow.  W's piece and x are
-// transposed beside it, so that every product is the same kernel's form (gemm_nt.h:
-// both operands along the reduction).  dx is summed over pieces in fp32.
+// (P for dx, its transpose for dW), and two products follow: P^T with x transposed
+// once (rows without part as zeros), P with W as it lies, through the transposing
+// LDS read.  dx is summed over pieces in fp32.
 // P in bf16 is the one rounding inside (2^-9 of an entry on average, independent
 // from entry to entry: 1.1e-3 of the gradients' norm beside their own rounding's
 // 1.7e-3); an entry of the target is p - 1 from fp32.
@@ -260,15 +260,16 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
 
 struct ProductArgs {
   const bf16_t* a;          // [M, lda]
-  const bf16_t* b;          // [N, ldb]
+  const bf16_t* b;          // [N, ldb], or (BT) [depth, N], rows past depth taken as zeros by A
   int M, N, K, lda, ldb;    // K a multiple of 64
+  int depth;
   int tiles_m, tiles_n, parts;
   bf16_t* out;              // [M, N] bf16 (parts == 1), or ...
   float* sums;              // ... [parts][M, N] fp32: part z of the reduction
   int add;                  // added to what sums holds
 };
 
-template <class S>
+template <class S, bool BT>
 __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_product_kernel(ProductArgs g) {
   __shared__ __attribute__((aligned(1024))) unsigned char smem[S::kLds];
   const int tiles = g.tiles_m * g.tiles_n;
@@ -280,8 +281,9 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
   const int m0 = tm * S::BM, n0 = tn * S::BN;
   f32x16 acc[S::MB][S::NB];
   const NtOperand a{g.a + static_cast<size_t>(m0) * g.lda + k0 * kNtBK, g.lda, g.M - m0};
-  const NtOperand b{g.b + static_cast<size_t>(n0) * g.ldb + k0 * kNtBK, g.ldb, g.N - n0};
-  gemm_nt<S>(a, b, (k1 - k0) * kNtBK, smem, acc);
+  const NtOperand b{BT ? g.b + static_cast<size_t>(k0) * kNtBK * g.ldb + n0 : g.b + static_cast<size_t>(n0) * g.ldb + k0 * kNtBK,
+                    g.ldb, g.N - n0, g.depth - k0 * kNtBK};
+  gemm_nt<S, BT>(a, b, (k1 - k0) * kNtBK, smem, acc);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int mw = m0 + 32 * S::MB * (wave / S::WC), nw = n0 + 32 * S::NB * (wave % S::WC);
@@ -376,14 +378,14 @@ unsigned blocks_for(int64_t items) {
 // What a backward pass holds: P and its transpose for a piece of the vocabulary of
 // about 2^27 entries (268 MB each; whole tiles; at least 8192 columns, under which
 // dx's fp32 sums, read and written once a piece, would cost a third of its product),
-// W's piece transposed, x transposed, dx's sums.
+// x transposed, dx's sums.
 struct Plan {
   int piece;                // columns of a piece, a multiple of 256
   int ldt;                  // rows, rounded up to 64
   Tile tile;                // of dx's product
   int parts;                // parts of its reduction
   bool sums;                // dx through fp32 sums
-  size_t p, pt, wt, xt, dx, bytes;
+  size_t p, pt, xt, dx, bytes;
 };
 
 int rows_of(Tile t) { return t == kRows32 ? 32 : (t == kRows64 ? 64 : (t == kMid ? 128 : 256)); }
@@ -441,11 +443,8 @@ Split pick_split(int64_t M, int64_t N, int64_t K) {
 Plan plan(int rows, int cols, int vocab) {
   Plan q{};
   q.ldt = up(rows, 64);
-  auto most = [](int64_t least, int64_t entries) { return entries > least ? entries : least; };
-  int64_t piece = most(8192, (int64_t{1} << 27) / q.ldt);
-  const int64_t by_w = most(2048, (int64_t{1} << 27) / cols);
-  if (by_w < piece) piece = by_w;
-  piece = piece / 256 * 256;
+  int64_t piece = (int64_t{1} << 27) / q.ldt / 256 * 256;
+  if (piece < 8192) piece = 8192;
   if (piece > up(vocab, 256)) piece = up(vocab, 256);
   q.piece = static_cast<int>(piece);
   const Split split = pick_split(rows, cols, q.piece);
@@ -460,7 +459,6 @@ Plan plan(int rows, int cols, int vocab) {
   };
   q.p = take(static_cast<size_t>(rows) * q.piece * 2);
   q.pt = take(static_cast<size_t>(q.piece) * q.ldt * 2);
-  q.wt = take(static_cast<size_t>(cols) * q.piece * 2);
   q.xt = take(static_cast<size_t>(cols) * q.ldt * 2);
   q.dx = take(q.sums ? static_cast<size_t>(q.parts) * rows * cols * 4 : 0);
   q.bytes = at;
@@ -482,11 +480,11 @@ void launch_probs(LogitArgs g, hipStream_t st) {
   head_probs_kernel<S><<<g.tiles_m * g.tiles_n, kNtThreads, 0, st>>>(g);
 }
 
-template <class S>
+template <class S, bool BT>
 void launch_product(ProductArgs g, hipStream_t st) {
   g.tiles_m = (g.M + S::BM - 1) / S::BM;
   g.tiles_n = (g.N + S::BN - 1) / S::BN;
-  head_product_kernel<S><<<g.tiles_m * g.tiles_n * g.parts, kNtThreads, 0, st>>>(g);
+  head_product_kernel<S, BT><<<g.tiles_m * g.tiles_n * g.parts, kNtThreads, 0, st>>>(g);
 }
 
 }  // namespace
@@ -531,7 +529,6 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   bf16_t* p = reinterpret_cast<bf16_t*>(ws + q.p);
   bf16_t* pt = reinterpret_cast<bf16_t*>(ws + q.pt);
-  bf16_t* wt = reinterpret_cast<bf16_t*>(ws + q.wt);
   bf16_t* xt = reinterpret_cast<bf16_t*>(ws + q.xt);
   float* sums = reinterpret_cast<float*>(ws + q.dx);
   const int col_tiles = (cols + 63) / 64;
@@ -566,24 +563,24 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
       d.lda = d.ldb = q.ldt;
       d.parts = 1;
       d.out = dw + static_cast<size_t>(v0) * cols;
-      with_tile(pick(d.M, d.N, d.K), [&](auto s) { launch_product<decltype(s)>(d, st); });
+      with_tile(pick(d.M, d.N, d.K), [&](auto s) { launch_product<decltype(s), false>(d, st); });
     }
     if (dx) {
-      head_transpose_kernel<<<col_tiles * (ldp / 64), 256, 0, st>>>(w + static_cast<size_t>(v0) * cols, v1 - v0, cols,
-                                                                    wt, ldp, nullptr, 0);
       ProductArgs d{};
       d.a = p;
-      d.b = wt;
+      d.b = w + static_cast<size_t>(v0) * cols;
       d.M = rows;
       d.N = cols;
       d.K = ldp;
-      d.lda = d.ldb = ldp;
+      d.lda = ldp;
+      d.ldb = cols;
+      d.depth = v1 - v0;                                   // (P's columns past it are zeros)
       const int most = ldp / kNtBK;
       d.parts = q.parts < most ? q.parts : most;
       d.out = dx;
       d.sums = q.sums ? sums : nullptr;
       d.add = v0 > 0;
-      with_tile(q.tile, [&](auto s) { launch_product<decltype(s)>(d, st); });
+      with_tile(q.tile, [&](auto s) { launch_product<decltype(s), true>(d, st); });
     }
     if (hipError_t e = hipGetLastError()) return e;
   }

@@ -333,3 +333,15 @@ def test_step_from_norm_to_update():
         say(f"{name}: {off:.2e}")
         assert off <= steps * b16, name
     assert torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("dx,dw", [(True, True), (True, False), (False, True)])
+def test_two_pieces(dx, dw):
+    # 2^27 / 16448 rows is under 8192 columns a piece: two pieces, the second ragged and
+    # shorter than the parts of dx's reduction would like
+    c = Case(16400, 8, 8203, seed=11)
+    c.forward()
+    c.backward(dx, dw)
+    torch.cuda.synchronize()
+    c.check_backward(dx, dw)
+    c.check_bands()
