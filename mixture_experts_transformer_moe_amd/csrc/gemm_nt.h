@@ -14,13 +14,13 @@
 //     next stage has landed: it was issued three steps before.
 //   * Rows past the last are the last row again (their results are not stored).
 //     K is a multiple of 8; pieces past its end read zeros.
-//   * BT: B lies the other way, the reduction along its columns' rows (B [K, N], N
-//     a multiple of 8).  A stage is then 64 of its rows, 16-byte units of row r
-//     XOR-swizzled by 4 (r mod 4), and gfx950's transposing LDS read hands a lane 4
-//     consecutive rows of one column, two reads an operand: in a group of 16 lanes
-//     it returns to lane 4a + b element b of the 8-byte pieces addressed by lanes a,
-//     a + 4, a + 8 and a + 12.  Rows past the reduction's end are its last one again:
-//     A has to hold zeros there.
+//   * AT, BT: that operand lies the other way, [K, its rows] with the reduction from
+//     row to row (its width a multiple of 8).  A stage is then 64 of its rows, 16-byte
+//     units of row r XOR-swizzled by 4 (r mod 4), and gfx950's transposing LDS read
+//     hands a lane 4 consecutive rows of one column, two reads an operand: in a group
+//     of 16 lanes it returns to lane 4a + b element b of the 8-byte pieces addressed
+//     by lanes a, a + 4, a + 8 and a + 12.  Rows past the reduction's end are its last
+//     one again: the other operand has to hold zeros there.
 #pragma once
 
 #include <type_traits>
@@ -46,10 +46,10 @@ struct NtShape {
 };
 
 struct NtOperand {
-  const bf16_t* p;     // the tile's first row (BT: its first column in row 0)
+  const bf16_t* p;     // the tile's first row (AT, BT: its first column in row 0)
   int ld;              // elements between rows, a multiple of 8
-  int rows;            // rows from p on that exist (>= 1; BT: columns, a multiple of 8)
-  int depth;           // BT: rows of the reduction that exist (>= 1)
+  int rows;            // rows from p on that exist (>= 1; AT, BT: columns, a multiple of 8)
+  int depth;           // AT, BT: rows of the reduction that exist (>= 1)
 };
 
 typedef short nt_v4i16 __attribute__((ext_vector_type(4)));
@@ -87,9 +87,10 @@ __device__ __forceinline__ void nt_each(F&& f, std::integer_sequence<int, Q...>)
   (f(std::integral_constant<int, Q>{}), ...);
 }
 
-template <class S, bool BT = false>
+template <class S, bool AT = false, bool BT = false>
 __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, int K, unsigned char* smem,
                                         f32x16 (&acc)[S::MB][S::NB]) {
+  static_assert((!AT || S::BM >= 128) && (!BT || S::BN >= 128), "the swizzle of transposed rows takes 16 units");
   constexpr int MB = S::MB, NB = S::NB;
   constexpr int NA = S::BM / 32, NBL = S::BN / 32;           // 1 KB loads of a wave and stage
   constexpr int NQ = NA + NBL;
@@ -100,23 +101,27 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
   const bool ragged = K % kNtBK != 0;
 
   // load q of a wave: rows 8 (NA wave + q) .. + 7 of A's tile, then the same of B's
-  // (BT: the stage's rows, 512 / BN of them a load)
-  constexpr int kBU = S::BN / 8;                             // BT: 16-byte units of a row
-  constexpr int kBR = 64 / kBU;                              // BT: rows of a load
-  auto bt_row = [&](int q) { return kBR * (NBL * wave + q - NA) + lane / kBU; };
-  auto bt_col = [&](int q) { return min(8 * ((lane % kBU) ^ (4 * (bt_row(q) & 3))), b.rows - 8); };
+  // (transposed: the stage's rows, 512 / BM or BN of them a load)
+  auto units = [](bool of_a) { return (of_a ? S::BM : S::BN) / 8; };   // 16-byte units of a transposed row
+  auto index = [&](int q) { return q < NA ? NA * wave + q : NBL * wave + q - NA; };
+  auto tr_row = [&](int q) { return 64 / units(q < NA) * index(q) + lane / units(q < NA); };
+  auto tr_col = [&](int q) {
+    return min(8 * ((lane % units(q < NA)) ^ (4 * (tr_row(q) & 3))), (q < NA ? a.rows : b.rows) - 8);
+  };
+  auto offset = [&](int r, int c, int ld) {
+    return (static_cast<uint32_t>(r) * static_cast<uint32_t>(ld) + static_cast<uint32_t>(c)) * 2u;
+  };
   uint32_t off[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     const bool of_a = q < NA;
-    if (BT && !of_a) {
-      off[q] = (static_cast<uint32_t>(bt_row(q)) * static_cast<uint32_t>(b.ld) + static_cast<uint32_t>(bt_col(q))) * 2u;
-      continue;
+    const int ld = of_a ? a.ld : b.ld;
+    if (of_a ? AT : BT) {
+      off[q] = offset(tr_row(q), tr_col(q), ld);
+    } else {
+      const int row = 8 * index(q) + (lane >> 3);
+      off[q] = offset(min(row, (of_a ? a.rows : b.rows) - 1), 8 * ((lane & 7) ^ nt_swizzle(row)), ld);
     }
-    const int row = 8 * (of_a ? NA * wave + q : NBL * wave + q - NA) + (lane >> 3);
-    const int piece = (lane & 7) ^ nt_swizzle(row);
-    const int r = min(row, (of_a ? a.rows : b.rows) - 1);
-    off[q] = (static_cast<uint32_t>(r) * static_cast<uint32_t>(of_a ? a.ld : b.ld) + 8u * piece) * 2u;
   }
   const unsigned char* pa = reinterpret_cast<const unsigned char*>(nt_uniform(a.p));
   const unsigned char* pb = reinterpret_cast<const unsigned char*>(nt_uniform(b.p));
@@ -124,23 +129,23 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
   // LDS: buffer s: A's rows, then B's
   auto issue = [&](int kb, int buf, auto q_tag, bool last) __attribute__((always_inline)) {
     constexpr int q = decltype(q_tag)::value;
-    constexpr bool of_a = q < NA;
-    const size_t step = BT && !of_a ? static_cast<size_t>(b.ld) * (kNtBK * 2) : kNtBK * 2;
-    const unsigned char* base = (of_a ? pa : pb) + kb * step;
+    constexpr bool of_a = q < NA, tr = of_a ? AT : BT;
+    const NtOperand& x = of_a ? a : b;
+    const unsigned char* base = (of_a ? pa : pb) + kb * (tr ? static_cast<size_t>(x.ld) * (kNtBK * 2) : kNtBK * 2);
     const uint32_t at = lds0 + static_cast<uint32_t>(buf) * S::kStage +
                         (of_a ? NA * 1024u * wave : S::BM * 128u + NBL * 1024u * wave);
-    if (BT && !of_a && last) {
-      const int row = min(bt_row(q), b.depth - 1 - kb * kNtBK);
-      const uint32_t o = (static_cast<uint32_t>(row) * static_cast<uint32_t>(b.ld) + static_cast<uint32_t>(bt_col(q))) * 2u;
-      nt_dma<(q - NA) * 1024>(base, o, __builtin_amdgcn_readfirstlane(at));
-    } else if (last && ragged) {
+    constexpr int kAt = (of_a ? q : q - NA) * 1024;
+    if (tr && last) {
+      nt_dma<kAt>(base, offset(min(tr_row(q), x.depth - 1 - kb * kNtBK), tr_col(q), x.ld),
+                  __builtin_amdgcn_readfirstlane(at));
+    } else if (!tr && last && ragged) {
       // the last stage of a ragged reduction: pieces past its end are zeros
-      const int row = 8 * (of_a ? NA * wave + q : NBL * wave + q - NA) + (lane >> 3);
+      const int row = 8 * index(q) + (lane >> 3);
       const int col = kb * kNtBK + 8 * ((lane & 7) ^ nt_swizzle(row));
       const void* from = col < K ? static_cast<const void*>(base + off[q]) : static_cast<const void*>(&kNtZeros);
-      dma16(from, __builtin_amdgcn_readfirstlane(at + (of_a ? q : q - NA) * 1024u));
+      dma16(from, __builtin_amdgcn_readfirstlane(at + kAt));
     } else {
-      nt_dma<(of_a ? q : q - NA) * 1024>(base, off[q], __builtin_amdgcn_readfirstlane(at));
+      nt_dma<kAt>(base, off[q], __builtin_amdgcn_readfirstlane(at));
     }
   };
   // the loads Q of a stage for which NM Q / NQ is k (all of them: k = -1)
@@ -160,24 +165,32 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
   struct Frag {
     u32x4 a[MB], b[NB];
   };
-  // BT: the lane's piece of row (lane / 16 / 2) 8 + (lane mod 16) / 4 of a step
-  uint32_t tr_off[NB];
-  if constexpr (BT) {
-    const int grp = lane >> 4, j = lane & 15;
+  // transposed: the lane's piece of row 8 (lane / 32) + (lane mod 16) / 4 of a step, by
+  // the operand's block
+  const int tgrp = lane >> 4, tj = lane & 15;
+  auto tr_at = [&](int block, int units) {
+    return static_cast<uint32_t>((8 * (tgrp >> 1) + (tj >> 2)) * (units * 16) +
+                                 (((4 * block + 2 * (tgrp & 1) + ((tj & 3) >> 1)) ^ (4 * (tj >> 2))) << 4) + 8 * (tj & 1));
+  };
+  uint32_t tr_a[MB], tr_b[NB];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-      tr_off[n] = static_cast<uint32_t>((8 * (grp >> 1) + (j >> 2)) * (kBU * 16) +
-                                        (((4 * (NB * wc + n) + 2 * (grp & 1) + ((j & 3) >> 1)) ^ (4 * (j >> 2))) << 4) +
-                                        8 * (j & 1));
-  }
+  for (int m = 0; m < MB; ++m) tr_a[m] = AT ? tr_at(MB * wr + m, S::BM / 8) : 0u;
+#pragma unroll
+  for (int n = 0; n < NB; ++n) tr_b[n] = BT ? tr_at(NB * wc + n, S::BN / 8) : 0u;
+  auto read_tr = [&](uint32_t at, int row_bytes, int s) __attribute__((always_inline)) {
+    const uint2 lo = nt_read_tr(at + 16 * s * row_bytes), hi = nt_read_tr(at + (16 * s + 4) * row_bytes);
+    return u32x4{lo.x, lo.y, hi.x, hi.y};
+  };
   auto read_one = [&](Frag& f, int buf, int s, int i) __attribute__((always_inline)) {
     const unsigned char* base = smem + buf * S::kStage;
-    if (BT && i < NB) {
-      const uint32_t at = lds0 + static_cast<uint32_t>(buf) * S::kStage + S::BM * 128u + 16u * s * (kBU * 16) + tr_off[i];
-      const uint2 lo = nt_read_tr(at), hi = nt_read_tr(at + 4 * (kBU * 16));
-      f.b[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
-    } else if (i < NB) f.b[i] = *reinterpret_cast<const u32x4*>(base + S::BM * 128 + (NB * wc + i) * 4096 + piece_off[s]);
-    else f.a[i - NB] = *reinterpret_cast<const u32x4*>(base + (MB * wr + i - NB) * 4096 + piece_off[s]);
+    const uint32_t at = lds0 + static_cast<uint32_t>(buf) * S::kStage;
+    if (i < NB) {
+      if constexpr (BT) f.b[i] = read_tr(at + S::BM * 128 + tr_b[i], S::BN * 2, s);
+      else f.b[i] = *reinterpret_cast<const u32x4*>(base + S::BM * 128 + (NB * wc + i) * 4096 + piece_off[s]);
+    } else {
+      if constexpr (AT) f.a[i - NB] = read_tr(at + tr_a[i - NB], S::BM * 2, s);
+      else f.a[i - NB] = *reinterpret_cast<const u32x4*>(base + (MB * wr + i - NB) * 4096 + piece_off[s]);
+    }
   };
   auto mfma = [&](const Frag& f, auto&& op) __attribute__((always_inline)) {
 #pragma unroll

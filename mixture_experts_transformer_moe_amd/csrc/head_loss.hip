@@ -10,13 +10,12 @@
 // Forward: a tile of z stays in the accumulators; each row's maximum and sum over
 // the tile's columns go out (8 bytes for 256 columns) and a second kernel joins
 // them in a fixed order.  Backward: the vocabulary goes by in pieces; per piece z
-// is computed again, P leaves the accumulators once as bf16, row-major both ways
-// (P for dx, its transpose for dW), and two products follow: P^T with x transposed
-// once (rows without part as zeros), P with W as it lies, through the transposing
-// LDS read.  dx is summed over pieces in fp32.
-// P in bf16 is the one rounding inside (2^-9 of an entry on average, independent
-// from entry to entry: 1.1e-3 of the gradients' norm beside their own rounding's
-// 1.7e-3); an entry of the target is p - 1 from fp32.
+// is computed again, P leaves the accumulators once as bf16, and two products follow,
+// each with one operand read across its rows (gemm_nt.h): P W, and P^T with x
+// transposed once (rows without part as zeros).  dx is summed over pieces in fp32.
+// P in bf16 is the one rounding inside: 1.7e-3 of an entry, independent from entry
+// to entry, so 2.3e-3 of the gradients' norm with their own rounding's 1.7e-3.  An
+// entry of the target is p - 1 from fp32.
 #include "head_loss.h"
 
 #include "gemm_nt.h"
@@ -95,8 +94,7 @@ struct LogitArgs {
   const float* lse;
   const float* dloss;
   bf16_t* p;                // [T, ldp]
-  bf16_t* pt;               // [v1 - v0, ldt]
-  int ldp, ldt;
+  int ldp;
 };
 
 template <class S>
@@ -224,43 +222,15 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
       asm volatile("" : "+a"(acc[m][n]));
     }
   }
-  constexpr int kTokB = 64 * S::MB;                        // bytes of the wave's rows, transposed
-  unsigned char* stg = smem + wave * (32 * S::NB * kTokB > 2048 * S::NB ? 32 * S::NB * kTokB : 2048 * S::NB);
-  static_assert(4 * (32 * S::NB * kTokB > 2048 * S::NB ? 32 * S::NB * kTokB : 2048 * S::NB) <= S::kLds, "LDS");
-  if (g.pt) {
-    // the transpose: columns as rows of 32 MB tokens
-#pragma unroll
-    for (int m = 0; m < S::MB; ++m)
-#pragma unroll
-      for (int n = 0; n < S::NB; ++n) {
-        asm volatile("" : "+a"(acc[m][n]));
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int v = 32 * n + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-          *reinterpret_cast<bf16_t*>(stg + v * kTokB + 2 * (32 * m + (lane & 31))) = f32_to_bf16(acc[m][n][r]);
-        }
-      }
-    __builtin_amdgcn_wave_barrier();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    constexpr int kPieces = kTokB / 16;
-#pragma unroll 4
-    for (int i = 0; i < 32 * S::NB * kPieces / 64; ++i) {
-      const int at = 64 * i + lane, v = at / kPieces, c = at % kPieces;
-      const u32x4 d = *reinterpret_cast<const u32x4*>(stg + v * kTokB + 16 * c);
-      if (vw + v < g.v1 && tw + 8 * c < g.ldt)
-        *(gu32x4*)((gbyte*)(g.pt + static_cast<size_t>(vw - g.v0 + v) * g.ldt + tw + 8 * c)) = d;
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-  }
-  if (g.p)
-    store_rows<S>(g.p + static_cast<size_t>(tw) * g.ldp + (vw - g.v0), g.ldp, g.T - tw, g.ldp - (vw - g.v0), stg,
-                  [&](int m, int n, int r) { return acc[m][n][r]; });
+  store_rows<S>(g.p + static_cast<size_t>(tw) * g.ldp + (vw - g.v0), g.ldp, g.T - tw, g.ldp - (vw - g.v0),
+                smem + wave * 2048 * S::NB, [&](int m, int n, int r) { return acc[m][n][r]; });
 }
 
+// dx: A = P [M, lda], B = W [depth, N]; dW (DW): A = P [depth, lda], B = x transposed
+// [N, ldb].  What is not transposed holds zeros past the reduction's end.
 struct ProductArgs {
-  const bf16_t* a;          // [M, lda]
-  const bf16_t* b;          // [N, ldb], or (BT) [depth, N], rows past depth taken as zeros by A
+  const bf16_t* a;
+  const bf16_t* b;
   int M, N, K, lda, ldb;    // K a multiple of 64
   int depth;
   int tiles_m, tiles_n, parts;
@@ -269,7 +239,7 @@ struct ProductArgs {
   int add;                  // added to what sums holds
 };
 
-template <class S, bool BT>
+template <class S, bool DW>
 __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_product_kernel(ProductArgs g) {
   __shared__ __attribute__((aligned(1024))) unsigned char smem[S::kLds];
   const int tiles = g.tiles_m * g.tiles_n;
@@ -280,10 +250,12 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
   const int k0 = static_cast<int>(static_cast<int64_t>(nk) * z / g.parts), k1 = static_cast<int>(static_cast<int64_t>(nk) * (z + 1) / g.parts);
   const int m0 = tm * S::BM, n0 = tn * S::BN;
   f32x16 acc[S::MB][S::NB];
-  const NtOperand a{g.a + static_cast<size_t>(m0) * g.lda + k0 * kNtBK, g.lda, g.M - m0};
-  const NtOperand b{BT ? g.b + static_cast<size_t>(k0) * kNtBK * g.ldb + n0 : g.b + static_cast<size_t>(n0) * g.ldb + k0 * kNtBK,
-                    g.ldb, g.N - n0, g.depth - k0 * kNtBK};
-  gemm_nt<S, BT>(a, b, (k1 - k0) * kNtBK, smem, acc);
+  const size_t kat = static_cast<size_t>(k0) * kNtBK;
+  const int depth = g.depth - k0 * kNtBK;
+  const NtOperand a{DW ? g.a + kat * g.lda + m0 : g.a + static_cast<size_t>(m0) * g.lda + kat, g.lda,
+                    (DW ? g.lda : g.M) - m0, depth};
+  const NtOperand b{DW ? g.b + static_cast<size_t>(n0) * g.ldb + kat : g.b + kat * g.ldb + n0, g.ldb, g.N - n0, depth};
+  gemm_nt<S, DW, !DW>(a, b, (k1 - k0) * kNtBK, smem, acc);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int mw = m0 + 32 * S::MB * (wave / S::WC), nw = n0 + 32 * S::NB * (wave % S::WC);
@@ -297,7 +269,8 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
   for (int m = 0; m < S::MB; ++m) {
     const int row = mw + 32 * m + (lane & 31);
 #pragma unroll
-    for (int n = 0; n < S::NB; ++n)
+    for (int n = 0; n < S::NB; ++n) {
+      if constexpr (S::MB * S::NB > 8) asm volatile("" : "+a"(acc[m][n]));   // one block at a time
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int col = nw + 32 * n + 8 * q + 4 * (lane >> 5);
@@ -310,6 +283,7 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
         }
         *at = v;
       }
+    }
   }
 }
 
@@ -385,7 +359,7 @@ struct Plan {
   Tile tile;                // of dx's product
   int parts;                // parts of its reduction
   bool sums;                // dx through fp32 sums
-  size_t p, pt, xt, dx, bytes;
+  size_t p, xt, dx, bytes;
 };
 
 int rows_of(Tile t) { return t == kRows32 ? 32 : (t == kRows64 ? 64 : (t == kMid ? 128 : 256)); }
@@ -407,12 +381,16 @@ double cost(Tile t, int64_t n, int64_t K) {
   return (n / 512 + (left == 0 ? 0.0 : (left <= 256 ? 0.65 : 1.0))) * (1.5 + 0.0150 * K);
 }
 
+Tile pick_square(int64_t M, int64_t N, int64_t K) {
+  return cost(kMid, tiles_of(kMid, M, N), K) < cost(kWide, tiles_of(kWide, M, N), K) ? kMid : kWide;
+}
+
 // The tile for an M x N product over K: low ones where the batch is that small
 // (bound by the reads of the other operand), else the cheaper of the two others.
-Tile pick(int64_t M, int64_t N, int64_t K, int lowest = 32) {
-  if (M <= 32 && lowest <= 32) return kRows32;
+Tile pick(int64_t M, int64_t N, int64_t K) {
+  if (M <= 32) return kRows32;
   if (M <= 64) return kRows64;
-  return cost(kMid, tiles_of(kMid, M, N), K) < cost(kWide, tiles_of(kWide, M, N), K) ? kMid : kWide;
+  return pick_square(M, N, K);
 }
 
 // dx's product: its tile, and the parts of its reduction that fill the CUs
@@ -458,7 +436,6 @@ Plan plan(int rows, int cols, int vocab) {
     return here;
   };
   q.p = take(static_cast<size_t>(rows) * q.piece * 2);
-  q.pt = take(static_cast<size_t>(q.piece) * q.ldt * 2);
   q.xt = take(static_cast<size_t>(cols) * q.ldt * 2);
   q.dx = take(q.sums ? static_cast<size_t>(q.parts) * rows * cols * 4 : 0);
   q.bytes = at;
@@ -480,11 +457,11 @@ void launch_probs(LogitArgs g, hipStream_t st) {
   head_probs_kernel<S><<<g.tiles_m * g.tiles_n, kNtThreads, 0, st>>>(g);
 }
 
-template <class S, bool BT>
+template <class S, bool DW>
 void launch_product(ProductArgs g, hipStream_t st) {
   g.tiles_m = (g.M + S::BM - 1) / S::BM;
   g.tiles_n = (g.N + S::BN - 1) / S::BN;
-  head_product_kernel<S, BT><<<g.tiles_m * g.tiles_n * g.parts, kNtThreads, 0, st>>>(g);
+  head_product_kernel<S, DW><<<g.tiles_m * g.tiles_n * g.parts, kNtThreads, 0, st>>>(g);
 }
 
 }  // namespace
@@ -528,7 +505,6 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
   const Plan q = plan(rows, cols, vocab);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   bf16_t* p = reinterpret_cast<bf16_t*>(ws + q.p);
-  bf16_t* pt = reinterpret_cast<bf16_t*>(ws + q.pt);
   bf16_t* xt = reinterpret_cast<bf16_t*>(ws + q.xt);
   float* sums = reinterpret_cast<float*>(ws + q.dx);
   const int col_tiles = (cols + 63) / 64;
@@ -547,23 +523,22 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
     g.v1 = v1;
     g.lse = lse;
     g.dloss = dloss;
-    g.p = dx ? p : nullptr;
-    g.pt = dw ? pt : nullptr;
+    g.p = p;
     g.ldp = ldp;
-    g.ldt = q.ldt;
-    // (64 rows at least: all ldt columns of the transpose have to be written)
-    with_tile(pick(rows, v1 - v0, cols, 64), [&](auto s) { launch_probs<decltype(s)>(g, st); });
+    with_tile(pick(rows, v1 - v0, cols), [&](auto s) { launch_probs<decltype(s)>(g, st); });
     if (dw) {
       ProductArgs d{};
-      d.a = pt;
+      d.a = p;
       d.b = xt;
       d.M = v1 - v0;
       d.N = cols;
-      d.K = q.ldt;
-      d.lda = d.ldb = q.ldt;
+      d.K = d.ldb = q.ldt;
+      d.lda = ldp;
+      d.depth = rows;
       d.parts = 1;
       d.out = dw + static_cast<size_t>(v0) * cols;
-      with_tile(pick(d.M, d.N, d.K), [&](auto s) { launch_product<decltype(s), false>(d, st); });
+      if (pick_square(d.M, d.N, d.K) == kMid) launch_product<Mid, true>(d, st);
+      else launch_product<Wide, true>(d, st);
     }
     if (dx) {
       ProductArgs d{};
@@ -580,7 +555,7 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
       d.out = dx;
       d.sums = q.sums ? sums : nullptr;
       d.add = v0 > 0;
-      with_tile(q.tile, [&](auto s) { launch_product<decltype(s), true>(d, st); });
+      with_tile(q.tile, [&](auto s) { launch_product<decltype(s), false>(d, st); });
     }
     if (hipError_t e = hipGetLastError()) return e;
   }
