@@ -234,12 +234,19 @@ struct ProductArgs {
   int M, N, K, lda, ldb;    // K a multiple of 64
   int depth;
   int tiles_m, tiles_n, parts;
-  bf16_t* out;              // [M, N] bf16 (parts == 1), or ...
-  float* sums;              // ... [parts][M, N] fp32: part z of the reduction
-  int add;                  // added to what sums holds
+  bf16_t* out;              // [M, N] bf16
+  float* sums;              // where the reduction comes in parts or pieces: fp32, as the
+                            // accumulators lie (whole kilobytes a wave and load)
+  int add, last;            // added to what sums holds; the last piece, straight to out
 };
 
-template <class S, bool DW>
+// where the sums of a wave's tile start, in float4
+template <class S>
+__device__ __forceinline__ size_t sums_at(int tile, int wave) {
+  return (static_cast<size_t>(tile) * 4 + wave) * (S::MB * S::NB * 256);
+}
+
+template <class S, bool DW, bool SUMS>
 __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_product_kernel(ProductArgs g) {
   __shared__ __attribute__((aligned(1024))) unsigned char smem[S::kLds];
   const int tiles = g.tiles_m * g.tiles_n;
@@ -259,45 +266,59 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int mw = m0 + 32 * S::MB * (wave / S::WC), nw = n0 + 32 * S::NB * (wave % S::WC);
-  if (g.sums == nullptr) {
-    store_rows<S>(g.out + static_cast<size_t>(mw) * g.N + nw, g.N, g.M - mw, g.N - nw, smem + wave * 2048 * S::NB,
-                  [&](int m, int n, int r) { return acc[m][n][r]; });
-    return;
-  }
-  float* sums = g.sums + static_cast<size_t>(z) * g.M * g.N;
+  bf16_t* out = g.out + static_cast<size_t>(mw) * g.N + nw;
+  auto rounded = [&]() __attribute__((always_inline)) {
+    store_rows<S>(out, g.N, g.M - mw, g.N - nw, smem + wave * 2048 * S::NB, [&](int m, int n, int r) { return acc[m][n][r]; });
+  };
+  if constexpr (!SUMS) {
+    rounded();
+  } else {
+    float4* sums = reinterpret_cast<float4*>(g.sums) + sums_at<S>((z * g.tiles_m + tm) * g.tiles_n + tn, wave) + lane;
 #pragma unroll
-  for (int m = 0; m < S::MB; ++m) {
-    const int row = mw + 32 * m + (lane & 31);
+    for (int m = 0; m < S::MB; ++m)
 #pragma unroll
-    for (int n = 0; n < S::NB; ++n) {
-      if constexpr (S::MB * S::NB > 8) asm volatile("" : "+a"(acc[m][n]));   // one block at a time
+      for (int n = 0; n < S::NB; ++n) {
+        if constexpr (S::MB * S::NB > 8) asm volatile("" : "+a"(acc[m][n]));   // one block at a time
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = nw + 32 * n + 8 * q + 4 * (lane >> 5);
-        if (row >= g.M || col >= g.N) continue;
-        float4* at = reinterpret_cast<float4*>(sums + static_cast<size_t>(row) * g.N + col);
-        float4 v = make_float4(acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]);
-        if (g.add) {
-          const float4 o = *at;
-          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        for (int q = 0; q < 4; ++q) {
+          float4* at = sums + ((m * S::NB + n) * 4 + q) * 64;
+          float4 v = make_float4(acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]);
+          if (g.add) {
+            const float4 o = *at;
+            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+          }
+          if (g.last) {
+            acc[m][n][4 * q] = v.x;
+            acc[m][n][4 * q + 1] = v.y;
+            acc[m][n][4 * q + 2] = v.z;
+            acc[m][n][4 * q + 3] = v.w;
+          } else {
+            *at = v;
+          }
         }
-        *at = v;
       }
-    }
+    if (g.last) rounded();
   }
 }
 
-// dx from the parts of its sum, in their order
-__global__ __launch_bounds__(256) void head_round_kernel(const float* sums, int parts, int64_t n, bf16_t* out) {
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < n;
-       i += static_cast<int64_t>(gridDim.x) * 1024) {
-    float4 v = *reinterpret_cast<const float4*>(sums + i);
-    for (int z = 1; z < parts; ++z) {
-      const float4 o = *reinterpret_cast<const float4*>(sums + z * n + i);
-      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-    }
-    *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+// dx from the parts of its sum, in their order: four values a thread
+template <class S>
+__global__ __launch_bounds__(256) void head_round_kernel(ProductArgs g) {
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;   // (a workgroup: one accumulator block)
+  const int block = blockIdx.x % (S::MB * S::NB), wave = blockIdx.x / (S::MB * S::NB) % 4;
+  const int tile = blockIdx.x / (4 * S::MB * S::NB);
+  const int m = block / S::NB, n = block % S::NB;
+  const int row = tile / g.tiles_n * S::BM + 32 * (S::MB * (wave / S::WC) + m) + (lane & 31);
+  const int col = tile % g.tiles_n * S::BN + 32 * (S::NB * (wave % S::WC) + n) + 8 * q + 4 * (lane >> 5);
+  if (row >= g.M || col >= g.N) return;
+  const float4* sums = reinterpret_cast<const float4*>(g.sums);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int z = 0; z < g.parts; ++z) {
+    const float4 o = sums[sums_at<S>(z * g.tiles_m * g.tiles_n + tile, wave) + (block * 4 + q) * 64 + lane];
+    v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
   }
+  *reinterpret_cast<uint2*>(g.out + static_cast<size_t>(row) * g.N + col) =
+      make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 // dst [cols, ldd] = src [rows, cols]^T in 64 x 64 tiles; columns of dst from rows to
@@ -437,7 +458,7 @@ Plan plan(int rows, int cols, int vocab) {
   };
   q.p = take(static_cast<size_t>(rows) * q.piece * 2);
   q.xt = take(static_cast<size_t>(cols) * q.ldt * 2);
-  q.dx = take(q.sums ? static_cast<size_t>(q.parts) * rows * cols * 4 : 0);
+  q.dx = take(q.sums ? static_cast<size_t>(q.parts) * tiles_of(q.tile, rows, cols) * rows_of(q.tile) * cols_of(q.tile) * 4 : 0);
   q.bytes = at;
   return q;
 }
@@ -461,7 +482,16 @@ template <class S, bool DW>
 void launch_product(ProductArgs g, hipStream_t st) {
   g.tiles_m = (g.M + S::BM - 1) / S::BM;
   g.tiles_n = (g.N + S::BN - 1) / S::BN;
-  head_product_kernel<S, DW><<<g.tiles_m * g.tiles_n * g.parts, kNtThreads, 0, st>>>(g);
+  const unsigned grid = g.tiles_m * g.tiles_n * g.parts;
+  if (!DW && g.sums) head_product_kernel<S, DW, !DW><<<grid, kNtThreads, 0, st>>>(g);
+  else head_product_kernel<S, DW, false><<<grid, kNtThreads, 0, st>>>(g);
+}
+
+template <class S>
+void launch_round(ProductArgs g, hipStream_t st) {
+  g.tiles_m = (g.M + S::BM - 1) / S::BM;
+  g.tiles_n = (g.N + S::BN - 1) / S::BN;
+  head_round_kernel<S><<<g.tiles_m * g.tiles_n * 4 * S::MB * S::NB, 256, 0, st>>>(g);
 }
 
 }  // namespace
@@ -550,18 +580,24 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
       d.lda = ldp;
       d.ldb = cols;
       d.depth = v1 - v0;                                   // (P's columns past it are zeros)
-      const int most = ldp / kNtBK;
-      d.parts = q.parts < most ? q.parts : most;
+      const int stages = ldp / kNtBK;                      // (a short last piece may have fewer than parts)
+      d.parts = q.parts < stages ? q.parts : stages;
       d.out = dx;
       d.sums = q.sums ? sums : nullptr;
       d.add = v0 > 0;
+      d.last = v1 == vocab && q.parts == 1;
       with_tile(q.tile, [&](auto s) { launch_product<decltype(s), false>(d, st); });
     }
     if (hipError_t e = hipGetLastError()) return e;
   }
-  if (dx && q.sums) {
-    const int64_t n = static_cast<int64_t>(rows) * cols;
-    head_round_kernel<<<blocks_for(n / 4), 256, 0, st>>>(sums, q.parts, n, dx);
+  if (dx && q.parts > 1) {
+    ProductArgs d{};
+    d.M = rows;
+    d.N = cols;
+    d.parts = q.parts;
+    d.out = dx;
+    d.sums = sums;
+    with_tile(q.tile, [&](auto s) { launch_round<decltype(s)>(d, st); });
   }
   return hipGetLastError();
 }
