@@ -728,8 +728,15 @@ hipError_t launch_tiles4(Int4Args a, int group, hipStream_t st) {
 
 template <int MODE>
 hipError_t launch_int4(const Int4Args& a, int group, hipStream_t st) {
+  // By the mean rows an expert.  The tile kernel spreads a weight's conversion over
+  // 128 rows but streams weights more slowly; scales of 32 columns cost it more.
+  // Measured at D = 4096, F = 1024 (groups of 128, us, rows kernel and tile kernel):
+  // gate/up 242, 304 at 16 rows, 299, 326 at 24, 385, 358 at 32; down (K = 1024) 139,
+  // 151 at 12, 165, 160 at 16, 193, 173 at 24; groups of 32: gate/up 433, 464 at 32,
+  // down 184, 200 at 16, 222, 212 at 24.
   const int mean = a.S / a.E;
-  if (mean >= 48) return launch_tiles4<MODE>(a, group, st);
+  const int tiles_from = MODE == kInt4GateUp ? (group == 32 ? 40 : 28) : (group == 32 ? 20 : 14);
+  if (mean >= tiles_from) return launch_tiles4<MODE>(a, group, st);
   if (mean >= 12) return launch_rows<MODE, 2>(a, group, st);
   return launch_rows<MODE, 1>(a, group, st);
 }
