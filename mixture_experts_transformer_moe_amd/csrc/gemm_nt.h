@@ -87,9 +87,10 @@ __device__ __forceinline__ void nt_each(F&& f, std::integer_sequence<int, Q...>)
   (f(std::integral_constant<int, Q>{}), ...);
 }
 
-template <class S, bool AT = false, bool BT = false>
+// pre(): run once the first two stages' loads are under way
+template <class S, bool AT = false, bool BT = false, class Pre>
 __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, int K, unsigned char* smem,
-                                        f32x16 (&acc)[S::MB][S::NB]) {
+                                        f32x16 (&acc)[S::MB][S::NB], Pre&& pre) {
   static_assert((!AT || S::BM >= 128) && (!BT || S::BN >= 128), "the swizzle of transposed rows takes 16 units");
   constexpr int MB = S::MB, NB = S::NB;
   constexpr int NA = S::BM / 32, NBL = S::BN / 32;           // 1 KB loads of a wave and stage
@@ -215,12 +216,10 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = f32x16{0.f};
   issue_at(0, 0, -1, nk == 1);
-  if (nk > 1) {
-    issue_at(1, 1, -1, nk == 2);
-    __builtin_amdgcn_s_waitcnt(vmcnt_only(NQ));
-  } else {
-    __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
-  }
+  if (nk > 1) issue_at(1, 1, -1, nk == 2);
+  pre();                                                      // (its loads only add to what the wait leaves out)
+  if (nk > 1) __builtin_amdgcn_s_waitcnt(vmcnt_only(NQ));
+  else __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   Frag f0, f1;

@@ -14,8 +14,11 @@
 // each with one operand read across its rows (gemm_nt.h): P W, and P^T with x
 // transposed once (rows without part as zeros).  dx is summed over pieces in fp32.
 // P in bf16 is the one rounding inside: 1.7e-3 of an entry, independent from entry
-// to entry, so 2.3e-3 of the gradients' norm with their own rounding's 1.7e-3.  An
-// entry of the target is p - 1 from fp32.
+// to entry.  The target's entry, p - 1 from fp32, is most of a row's norm, and its
+// rounding is common to all of the row: what it lost is kept in fp32 and added to
+// both products (333 x 1000 over 33001: 2.4e-3 of the gradients' norm without it, up
+// to 3.4e-3 for single rows, 1.66e-3 with it, which is their own rounding; 3% of the
+// time at 8192 x 4096 over 100352, 9% at 256 rows).
 #include "head_loss.h"
 
 #include "gemm_nt.h"
@@ -25,6 +28,8 @@ namespace {
 
 typedef __attribute__((address_space(1))) unsigned char gbyte;
 typedef __attribute__((address_space(1))) u32x4 gu32x4;
+
+constexpr int kOrderCols = 128;
 
 // Tiles: 256 x 256 with one workgroup a CU, 128 x 128 with two, and low ones that
 // leave small batches bound by the weights.
@@ -94,6 +99,7 @@ struct LogitArgs {
   const float* lse;
   const float* dloss;
   bf16_t* p;                // [T, ldp]
+  float* rest;              // [T]: what the target's entry of P lost to bf16
   int ldp;
 };
 
@@ -105,7 +111,7 @@ __device__ __forceinline__ void logits_tile(const LogitArgs& g, unsigned char* s
   v0 = g.v0 + tn * S::BN;
   const NtOperand a{g.x + static_cast<size_t>(t0) * g.D, g.D, g.T - t0};
   const NtOperand b{g.w + static_cast<size_t>(v0) * g.D, g.D, g.V - v0};
-  gemm_nt<S>(a, b, g.D, smem, acc);
+  gemm_nt<S>(a, b, g.D, smem, acc, [] {});
 }
 
 template <class S>
@@ -209,6 +215,7 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
     const int y = g.target[tc];
     const bool takes = t < g.T && y >= 0 && y < g.V;
     const float lse = g.lse[tc], w = g.dloss[tc];
+    float mine = 0.0f;                                     // the target's entry, where this lane holds it
 #pragma unroll
     for (int n = 0; n < S::NB; ++n) {
       asm volatile("" : "+a"(acc[m][n]));
@@ -217,10 +224,15 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
         const int v = vw + 32 * n + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
         float p = __expf(acc[m][n][r] - lse);
         if (v == y) p -= 1.0f;
-        acc[m][n][r] = takes && v < g.V ? p * w : 0.0f;
+        p = takes && v < g.V ? p * w : 0.0f;
+        mine = v == y ? p : mine;
+        acc[m][n][r] = p;
       }
       asm volatile("" : "+a"(acc[m][n]));
     }
+    const int at = y - vw;
+    if (takes && at >= 0 && at < 32 * S::NB && (at >> 2 & 1) == lane >> 5)
+      g.rest[t] = mine - bf16_to_f32(f32_to_bf16(mine));
   }
   store_rows<S>(g.p + static_cast<size_t>(tw) * g.ldp + (vw - g.v0), g.ldp, g.T - tw, g.ldp - (vw - g.v0),
                 smem + wave * 2048 * S::NB, [&](int m, int n, int r) { return acc[m][n][r]; });
@@ -238,6 +250,14 @@ struct ProductArgs {
   float* sums;              // where the reduction comes in parts or pieces: fp32, as the
                             // accumulators lie (whole kilobytes a wave and load)
   int add, last;            // added to what sums holds; the last piece, straight to out
+  // the target's entries of P, whose rounding is made good
+  const int32_t* target;    // [T]
+  const float* rest;        // [T]
+  int T, v0, v1;            // the piece's columns of P
+  const bf16_t* x;          // DW: [T, N], and its rows in order of their targets (head_order_kernel)
+  const int32_t* order;
+  const int32_t* order_at;
+  int order_groups;
 };
 
 // where the sums of a wave's tile start, in float4
@@ -262,10 +282,109 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
   const NtOperand a{DW ? g.a + kat * g.lda + m0 : g.a + static_cast<size_t>(m0) * g.lda + kat, g.lda,
                     (DW ? g.lda : g.M) - m0, depth};
   const NtOperand b{DW ? g.b + static_cast<size_t>(n0) * g.ldb + kat : g.b + kat * g.ldb + n0, g.ldb, g.N - n0, depth};
-  gemm_nt<S, DW, !DW>(a, b, (k1 - k0) * kNtBK, smem, acc);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int mw = m0 + 32 * S::MB * (wave / S::WC), nw = n0 + 32 * S::NB * (wave % S::WC);
+  const int wr = wave / S::WC, wc = wave % S::WC;
+  const int mw = m0 + 32 * S::MB * wr, nw = n0 + 32 * S::NB * wc;
+
+  // What the targets' entries of P lost, read ahead of the reduction.  DW: the tile's
+  // list of rows with a target among its columns, 16 at a time as 16 more values of
+  // the reduction, in bf16 (a target's entry then has 16 bits).
+  struct Lost {
+    int row[8];             // the column of P in the tile, -1: none
+    float rest[8];
+    bf16x8 x[S::NB];
+  } lost;
+  int list_at = 0, list_end = 0;
+  // (scalar loads: a vector load's wait would count the stages under way)
+  typedef const __attribute__((address_space(4))) int32_t* Scalars;
+  auto load_lost = [&](int e) __attribute__((always_inline)) {
+    int entries[16];                                       // (past the list's end: still in the workspace)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) entries[i] = ((Scalars)(g.order))[e + i];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = e + 8 * (lane >> 5) + j;
+      const int entry = i < list_end ? (lane < 32 ? entries[j] : entries[8 + j]) : -1;
+      const int t = entry < 0 ? 0 : entry >> 8;
+      lost.row[j] = entry < 0 ? -1 : entry & (S::BM - 1);
+      lost.rest[j] = entry < 0 ? 0.0f : g.rest[t];
+#pragma unroll
+      for (int n = 0; n < S::NB; ++n) {
+        const int col = nw + 32 * n + (lane & 31);
+        const bool in = entry >= 0 && col < g.N;
+        lost.x[n][j] = __builtin_bit_cast(__bf16, in ? g.x[static_cast<size_t>(t) * g.N + col] : bf16_t{0});
+      }
+    }
+  };
+  // (dx: each row's target and what its entry lost, where this piece holds it)
+  int to[S::MB];
+  float rest[S::MB];
+  gemm_nt<S, DW, !DW>(a, b, (k1 - k0) * kNtBK, smem, acc, [&]() __attribute__((always_inline)) {
+    if constexpr (DW) {
+      const int first = (g.v0 + m0) / kOrderCols;
+      list_at = ((Scalars)(g.order_at))[first];
+      list_end = ((Scalars)(g.order_at))[min(first + S::BM / kOrderCols, g.order_groups)];
+      if (list_at < list_end) load_lost(list_at);
+    } else {
+#pragma unroll
+      for (int m = 0; m < S::MB; ++m) {
+        const int t = mw + 32 * m + (lane & 31);
+        const int v = z == 0 && t < g.T ? g.target[t] : -1;
+        to[m] = v >= g.v0 && v < g.v1 ? v - g.v0 : -1;
+        rest[m] = to[m] >= 0 ? g.rest[t] : 0.0f;
+      }
+    }
+  });
+  if constexpr (DW) {
+    for (int e = list_at; e < list_end;) {
+      bf16x8 r[S::MB];
+#pragma unroll
+      for (int m = 0; m < S::MB; ++m)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          r[m][j] = __builtin_bit_cast(
+              __bf16, lost.row[j] == 32 * (S::MB * wr + m) + (lane & 31) ? f32_to_bf16(lost.rest[j]) : bf16_t{0});
+#pragma unroll
+      for (int m = 0; m < S::MB; ++m)
+#pragma unroll
+        for (int n = 0; n < S::NB; ++n)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lost.x[n], r[m], acc[m][n], 0, 0, 0);
+      e += 16;
+      if (e < list_end) load_lost(e);
+    }
+  } else if (z == 0) {
+    // row t takes rest[t] times its target's row of W
+#pragma unroll
+    for (int m = 0; m < S::MB; ++m) {
+      const bf16_t* row = g.b + static_cast<size_t>(max(to[m], 0)) * g.ldb;
+#pragma unroll
+      for (int n0 = 0; n0 < S::NB; n0 += 2) {
+        uint2 w[2][4];                                     // (two blocks' loads at a time)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = nw + 32 * (n0 + i) + 8 * q + 4 * (lane >> 5);
+            w[i][q] = to[m] >= 0 && col < g.N ? *reinterpret_cast<const uint2*>(row + col) : make_uint2(0u, 0u);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f32x16& c = acc[m][n0 + i];
+          if constexpr (S::MB * S::NB > 8) asm volatile("" : "+a"(c));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            c[4 * q] = fmaf(rest[m], __uint_as_float(w[i][q].x << 16), c[4 * q]);
+            c[4 * q + 1] = fmaf(rest[m], __uint_as_float(w[i][q].x & 0xffff0000u), c[4 * q + 1]);
+            c[4 * q + 2] = fmaf(rest[m], __uint_as_float(w[i][q].y << 16), c[4 * q + 2]);
+            c[4 * q + 3] = fmaf(rest[m], __uint_as_float(w[i][q].y & 0xffff0000u), c[4 * q + 3]);
+          }
+          if constexpr (S::MB * S::NB > 8) asm volatile("" : "+a"(c));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
   bf16_t* out = g.out + static_cast<size_t>(mw) * g.N + nw;
   auto rounded = [&]() __attribute__((always_inline)) {
     store_rows<S>(out, g.N, g.M - mw, g.N - nw, smem + wave * 2048 * S::NB, [&](int m, int n, int r) { return acc[m][n][r]; });
@@ -319,6 +438,55 @@ __global__ __launch_bounds__(256) void head_round_kernel(ProductArgs g) {
   }
   *reinterpret_cast<uint2*>(g.out + static_cast<size_t>(row) * g.N + col) =
       make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// The rows of a batch by the 128-column group of their target, in order within it:
+// order[i] = row << 8 | target mod 256, order_at[g] the first of group g.  A workgroup
+// a group: the targets of lower groups give its place, then each wave writes the
+// matches of its quarter of the batch.
+__global__ __launch_bounds__(256) void head_order_kernel(const int32_t* target, int T, int V, int32_t* order,
+                                                         int32_t* order_at) {
+  __shared__ int less_of[4], own_of[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int group = blockIdx.x, v0 = group * kOrderCols, v1 = min(v0 + kOrderCols, V);
+  const int quarter = (T + 255) / 256 * 64;
+  const int from = wave * quarter, to = min(from + quarter, T);
+  int less = 0, own = 0;
+#pragma unroll 8
+  for (int t = from + lane; t < to; t += 64) {
+    const int y = target[t];
+    less += y >= 0 && y < v0;
+    own += y >= v0 && y < v1;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    less += __shfl_xor(less, o);
+    own += __shfl_xor(own, o);
+  }
+  if (lane == 0) {
+    less_of[wave] = less;
+    own_of[wave] = own;
+  }
+  __syncthreads();
+  const int start = less_of[0] + less_of[1] + less_of[2] + less_of[3];
+  int at = start, all = start;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) at += own_of[w];
+    all += own_of[w];
+  }
+  if (threadIdx.x == 0) {
+    order_at[group] = start;
+    if (v1 == V) order_at[group + 1] = all;
+  }
+  if (own_of[wave] == 0) return;
+  for (int i = from; i < to; i += 64) {
+    const int t = i + lane;
+    const int y = t < to ? target[t] : -1;
+    const bool here = y >= v0 && y < v1;
+    const uint64_t mask = __ballot(here);
+    if (here) order[at + __popcll(mask & ((uint64_t{1} << lane) - 1))] = t << 8 | (y & 255);
+    at += __popcll(mask);
+  }
 }
 
 // dst [cols, ldd] = src [rows, cols]^T in 64 x 64 tiles; columns of dst from rows to
@@ -380,7 +548,7 @@ struct Plan {
   Tile tile;                // of dx's product
   int parts;                // parts of its reduction
   bool sums;                // dx through fp32 sums
-  size_t p, xt, dx, bytes;
+  size_t p, xt, dx, rest, order, order_at, bytes;
 };
 
 int rows_of(Tile t) { return t == kRows32 ? 32 : (t == kRows64 ? 64 : (t == kMid ? 128 : 256)); }
@@ -459,6 +627,9 @@ Plan plan(int rows, int cols, int vocab) {
   q.p = take(static_cast<size_t>(rows) * q.piece * 2);
   q.xt = take(static_cast<size_t>(cols) * q.ldt * 2);
   q.dx = take(q.sums ? static_cast<size_t>(q.parts) * tiles_of(q.tile, rows, cols) * rows_of(q.tile) * cols_of(q.tile) * 4 : 0);
+  q.rest = take(static_cast<size_t>(rows) * 4);
+  q.order = take(static_cast<size_t>(rows) * 4);
+  q.order_at = take((static_cast<size_t>(vocab) / kOrderCols + 2) * 4);
   q.bytes = at;
   return q;
 }
@@ -537,7 +708,12 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
   bf16_t* p = reinterpret_cast<bf16_t*>(ws + q.p);
   bf16_t* xt = reinterpret_cast<bf16_t*>(ws + q.xt);
   float* sums = reinterpret_cast<float*>(ws + q.dx);
+  float* rest = reinterpret_cast<float*>(ws + q.rest);
+  int32_t* order = reinterpret_cast<int32_t*>(ws + q.order);
+  int32_t* order_at = reinterpret_cast<int32_t*>(ws + q.order_at);
+  const int order_groups = (vocab + kOrderCols - 1) / kOrderCols;
   const int col_tiles = (cols + 63) / 64;
+  if (dw) head_order_kernel<<<order_groups, 256, 0, st>>>(target, rows, vocab, order, order_at);
   if (dw) head_transpose_kernel<<<col_tiles * (q.ldt / 64), 256, 0, st>>>(x, rows, cols, xt, q.ldt, target, vocab);
   for (int v0 = 0; v0 < vocab; v0 += q.piece) {
     const int v1 = vocab - v0 < q.piece ? vocab : v0 + q.piece;
@@ -554,10 +730,21 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
     g.lse = lse;
     g.dloss = dloss;
     g.p = p;
+    g.rest = rest;
     g.ldp = ldp;
+    ProductArgs base{};
+    base.target = target;
+    base.rest = rest;
+    base.x = x;
+    base.T = rows;
+    base.order = order;
+    base.order_at = order_at;
+    base.order_groups = order_groups;
+    base.v0 = v0;
+    base.v1 = v1;
     with_tile(pick(rows, v1 - v0, cols), [&](auto s) { launch_probs<decltype(s)>(g, st); });
     if (dw) {
-      ProductArgs d{};
+      ProductArgs d = base;
       d.a = p;
       d.b = xt;
       d.M = v1 - v0;
@@ -571,7 +758,7 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
       else launch_product<Wide, true>(d, st);
     }
     if (dx) {
-      ProductArgs d{};
+      ProductArgs d = base;
       d.a = p;
       d.b = w + static_cast<size_t>(v0) * cols;
       d.M = rows;
