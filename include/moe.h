@@ -604,7 +604,9 @@ int moe_orthogonalize(int64_t count, int32_t rows, int32_t cols, int32_t dtype, 
  * MOE_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------- */
 
-/* Bytes of workspace both calls need (0 for sizes they reject, and for rows == 0). */
+/* Bytes of workspace both calls need (0 for sizes they reject, and for rows == 0).
+ * Does not shrink as rows grow: the workspace of the largest batch serves the smaller
+ * ones of the same head. */
 size_t moe_head_loss_workspace_bytes(int64_t rows, int32_t cols, int32_t vocab);
 
 /* Forward.
@@ -627,8 +629,8 @@ int moe_head_loss_forward(int64_t rows, int32_t cols, int32_t vocab, int32_t dty
  *           (not computed), not both
  *   workspace as for the forward pass
  * The vocabulary goes by in pieces, each piece's logits computed again.  P is
- * rounded to bf16 for the two products, dx and dw once more.  All sums run in a
- * fixed order: the results are bit-reproducible.  rows == 0 writes zeros to dw.
+ * rounded to bf16 for the two products (the target's entry is held in more), dx and
+ * dw once more.  All sums run in a fixed order: the results are bit-reproducible.  rows == 0 writes zeros to dw.
  * Outputs must not overlap the other arguments.  The workspace holds nothing between
  * calls; calls and captured graphs that may run at the same time need one each. */
 int moe_head_loss_backward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,

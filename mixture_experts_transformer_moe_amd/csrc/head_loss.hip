@@ -668,11 +668,21 @@ void launch_round(ProductArgs g, hipStream_t st) {
 }  // namespace
 
 size_t head_loss_workspace_bytes(int64_t rows, int cols, int vocab) {
-  const size_t parts = (vocab + 127) / 128;                 // (of the narrowest tile)
-  const size_t forward = static_cast<size_t>(rows) * (parts * 8 + 4) + 512;
-  const size_t backward = plan(static_cast<int>(rows), cols, vocab).bytes;
-  const size_t n = forward > backward ? forward : backward;
-  return (n + 255) / 256 * 256;
+  // Bounds of what the forward pass and a plan take that do not shrink as rows grow
+  // (a plan's own sizes may: more rows can take shorter pieces and fewer parts).
+  const size_t n = static_cast<size_t>(rows), V = static_cast<size_t>(up(vocab, 256));
+  const size_t tiles = static_cast<size_t>(up(static_cast<int>(rows), 256)) * up(cols, 256);
+  auto least = [](size_t a, size_t b) { return a < b ? a : b; };
+  auto most = [](size_t a, size_t b) { return a > b ? a : b; };
+  auto padded = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
+  const size_t p = least(n * V, most(size_t{1} << 27, n * 8192)) * 2;
+  // one part a tile, or as many as the CUs hold (at most 256 x 256 values each) with
+  // 1024 columns each
+  const size_t dx = most(tiles, least(size_t{256} << 16, tiles * (V / 1024))) * 4;
+  const size_t backward = padded(p) + padded(static_cast<size_t>(cols) * up(static_cast<int>(rows), 64) * 2) + padded(dx) +
+                          2 * padded(n * 4) + padded((static_cast<size_t>(vocab) / kOrderCols + 2) * 4);
+  const size_t forward = n * ((vocab + 127) / 128 * size_t{8} + 4) + 512;    // (128: the narrowest tile's columns)
+  return padded(most(forward, backward));
 }
 
 hipError_t launch_head_loss_forward(int rows, int cols, int vocab, const bf16_t* x, const bf16_t* w,

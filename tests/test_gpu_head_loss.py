@@ -345,3 +345,46 @@ def test_two_pieces(dx, dw):
     torch.cuda.synchronize()
     c.check_backward(dx, dw)
     c.check_bands()
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(400, 64, 3), (90, 256, 2), (600, 72, 130)])
+def test_many_rows_with_one_target(rows, cols, vocab):
+    c = Case(rows, cols, vocab, ignored=0.1, seed=12)
+    c.y[c.y >= 0] = vocab - 1
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    c.check_forward()
+    c.check_backward()
+    c.check_bands()
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(1, 512, 3000), (6, 256, 2000), (70, 384, 5000), (300, 512, 4000)])
+def test_target_entries_are_held_finer(rows, cols, vocab):
+    # rows of nearly uniform probabilities: the target's entry is all but the whole
+    # gradient, and held in 16 bits.  What is left is the outputs' own rounding, b / sqrt 3
+    # of a value at most on average, and that of entries whose squares sum to 1 / vocab
+    # of the target's
+    for seed in range(4):
+        c = Case(rows, cols, vocab, ignored=0.0, seed=20 + seed, scale=0.05)
+        c.forward()
+        c.backward()
+        torch.cuda.synchronize()
+        x, w, y = to_f64(c.x), to_f64(c.w), c.y.cpu().numpy()
+        dx, dw = O.backward(x, w, y, to_f64(c.lse), to_f64(c.g))
+        for got, want in ((c.dx, dx), (c.dw, dw)):
+            off = np.linalg.norm(to_f64(got) - want) / np.linalg.norm(want)
+            assert off <= b16 / 3 ** 0.5 * (1 + 4 / vocab ** 0.5), (seed, off)
+
+
+def test_a_larger_batch_s_workspace():
+    c = Case(40, 128, 3000, seed=13)
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in c.guards]
+    c.work = torch.full((M.moe_head_loss_workspace_bytes(700, 128, 3000),), 255, dtype=torch.uint8, device="cuda")
+    c.forward()
+    c.backward()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, c.guards))

@@ -118,3 +118,9 @@ def test_binding_checks_tensors():
         M.moe_head_loss_forward(x, w[:, :8].contiguous(), y, f, f.clone(), None)     # another width
     with pytest.raises(ValueError):
         M.moe_head_loss_forward(x, w, y.long(), f, f.clone(), None)                  # another type
+
+
+def test_workspace_does_not_shrink(L):
+    for cols, vocab in ((4096, 100352), (1000, 33001), (8, 9000), (65536, 3)):
+        sizes = [L.moe_head_loss_workspace_bytes(rows, cols, vocab) for rows in range(1, 40000, 97)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
