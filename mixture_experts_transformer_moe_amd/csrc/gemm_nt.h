@@ -60,6 +60,20 @@ __device__ __forceinline__ uint2 nt_read_tr(uint32_t at) {
                                        (lds_v4*)(reinterpret_cast<__attribute__((address_space(3))) bf16_t*>(at))));
 }
 
+// a lane's piece of a transposed stage with rows of `units` 16-byte units: row 8 (lane /
+// 32) + (lane mod 16) / 4 of a step, by the operand's block of 32 columns
+__device__ __forceinline__ uint32_t nt_tr_at(int lane, int block, int units) {
+  const int tgrp = lane >> 4, tj = lane & 15;
+  return static_cast<uint32_t>((8 * (tgrp >> 1) + (tj >> 2)) * (units * 16) +
+                               (((4 * block + 2 * (tgrp & 1) + ((tj & 3) >> 1)) ^ (4 * (tj >> 2))) << 4) + 8 * (tj & 1));
+}
+
+// the operand of 16-wide step s of such a stage
+__device__ __forceinline__ u32x4 nt_read_step(uint32_t at, int row_bytes, int s) {
+  const uint2 lo = nt_read_tr(at + 16 * s * row_bytes), hi = nt_read_tr(at + (16 * s + 4) * row_bytes);
+  return u32x4{lo.x, lo.y, hi.x, hi.y};
+}
+
 // a pointer that is the same in every lane, made visibly so
 template <typename T>
 __device__ __forceinline__ const T* nt_uniform(const T* p) {
@@ -166,30 +180,19 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
   struct Frag {
     u32x4 a[MB], b[NB];
   };
-  // transposed: the lane's piece of row 8 (lane / 32) + (lane mod 16) / 4 of a step, by
-  // the operand's block
-  const int tgrp = lane >> 4, tj = lane & 15;
-  auto tr_at = [&](int block, int units) {
-    return static_cast<uint32_t>((8 * (tgrp >> 1) + (tj >> 2)) * (units * 16) +
-                                 (((4 * block + 2 * (tgrp & 1) + ((tj & 3) >> 1)) ^ (4 * (tj >> 2))) << 4) + 8 * (tj & 1));
-  };
   uint32_t tr_a[MB], tr_b[NB];
 #pragma unroll
-  for (int m = 0; m < MB; ++m) tr_a[m] = AT ? tr_at(MB * wr + m, S::BM / 8) : 0u;
+  for (int m = 0; m < MB; ++m) tr_a[m] = AT ? nt_tr_at(lane, MB * wr + m, S::BM / 8) : 0u;
 #pragma unroll
-  for (int n = 0; n < NB; ++n) tr_b[n] = BT ? tr_at(NB * wc + n, S::BN / 8) : 0u;
-  auto read_tr = [&](uint32_t at, int row_bytes, int s) __attribute__((always_inline)) {
-    const uint2 lo = nt_read_tr(at + 16 * s * row_bytes), hi = nt_read_tr(at + (16 * s + 4) * row_bytes);
-    return u32x4{lo.x, lo.y, hi.x, hi.y};
-  };
+  for (int n = 0; n < NB; ++n) tr_b[n] = BT ? nt_tr_at(lane, NB * wc + n, S::BN / 8) : 0u;
   auto read_one = [&](Frag& f, int buf, int s, int i) __attribute__((always_inline)) {
     const unsigned char* base = smem + buf * S::kStage;
     const uint32_t at = lds0 + static_cast<uint32_t>(buf) * S::kStage;
     if (i < NB) {
-      if constexpr (BT) f.b[i] = read_tr(at + S::BM * 128 + tr_b[i], S::BN * 2, s);
+      if constexpr (BT) f.b[i] = nt_read_step(at + S::BM * 128 + tr_b[i], S::BN * 2, s);
       else f.b[i] = *reinterpret_cast<const u32x4*>(base + S::BM * 128 + (NB * wc + i) * 4096 + piece_off[s]);
     } else {
-      if constexpr (AT) f.a[i - NB] = read_tr(at + tr_a[i - NB], S::BM * 2, s);
+      if constexpr (AT) f.a[i - NB] = nt_read_step(at + tr_a[i - NB], S::BM * 2, s);
       else f.a[i - NB] = *reinterpret_cast<const u32x4*>(base + (MB * wr + i - NB) * 4096 + piece_off[s]);
     }
   };
@@ -253,11 +256,15 @@ __device__ __forceinline__ void gemm_nt(const NtOperand& a, const NtOperand& b, 
 // Tile order for 8 XCDs (workgroup b runs on XCD b mod 8): each XCD takes a run of
 // consecutive tiles, and consecutive tiles are blocks of 4 row tiles of A by the
 // column tiles, so that the 32 tiles that run on an XCD at a time share 4 panels
-// of A and 8 of B behind one L2.
-__device__ __forceinline__ void nt_tile(int b, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int n = tiles_m * tiles_n;
+// of A and 8 of B behind one L2.  Where a reduction comes in parts the run goes
+// through the tiles of part z, then of the next: they share the part's panels (dx of 333
+// rows x 1000 in 21 parts of 33001: 30 us, 48 with a part's 24 tiles spread over the XCDs).
+__device__ __forceinline__ void nt_tile(int b, int tiles_m, int tiles_n, int parts, int& tm, int& tn, int& z) {
+  const int tiles = tiles_m * tiles_n, n = tiles * parts;
   const int x = b % 8, i = b / 8, q = n / 8, rem = n % 8;
-  const int t = x * q + min(x, rem) + i;
+  int t = x * q + min(x, rem) + i;
+  z = t / tiles;
+  t -= z * tiles;
   const int group = t / (4 * tiles_n), m0 = 4 * group;
   const int gm = min(4, tiles_m - m0), in = t - group * 4 * tiles_n;
   tm = m0 + in % gm;

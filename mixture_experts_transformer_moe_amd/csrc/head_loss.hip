@@ -105,8 +105,8 @@ struct LogitArgs {
 
 template <class S>
 __device__ __forceinline__ void logits_tile(const LogitArgs& g, unsigned char* smem, int& t0, int& v0, f32x16 (&acc)[S::MB][S::NB]) {
-  int tm, tn;
-  nt_tile(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+  int tm, tn, z;
+  nt_tile(blockIdx.x, g.tiles_m, g.tiles_n, 1, tm, tn, z);
   t0 = tm * S::BM;
   v0 = g.v0 + tn * S::BN;
   const NtOperand a{g.x + static_cast<size_t>(t0) * g.D, g.D, g.T - t0};
@@ -254,7 +254,7 @@ struct ProductArgs {
   const int32_t* target;    // [T]
   const float* rest;        // [T]
   int T, v0, v1;            // the piece's columns of P
-  const bf16_t* x;          // DW: [T, N], and its rows in order of their targets (head_order_kernel)
+  const bf16_t* x;          // DW: [T, N], and its rows in order of their targets (order_rows)
   const int32_t* order;
   const int32_t* order_at;
   int order_groups;
@@ -266,13 +266,83 @@ __device__ __forceinline__ size_t sums_at(int tile, int wave) {
   return (static_cast<size_t>(tile) * 4 + wave) * (S::MB * S::NB * 256);
 }
 
+// dW: the entries from .. to - 1 of a tile's list, 64 at a time as a stage of the
+// reduction.  Their rows of x go to LDS by direct loads, two stages deep, laid out as
+// gemm_nt.h has an operand that is read across its rows; the other operand holds an
+// entry's value where its column is the lane's.  Frequent targets and small
+// vocabularies make such lists: 16384 x 2048 over 500 lists of 4096, whose gradients
+// take 357 us (1179 with 16 entries at a time by ordinary loads), 8192 x 4096 over 8192
+// of 256, 1371 us (1572).
+template <class S>
+__device__ __forceinline__ void add_listed(const ProductArgs& g, int from, int to, int n0, unsigned char* smem,
+                                           f32x16 (&acc)[S::MB][S::NB]) {
+  constexpr int kList = 64, kBuf = kList * S::BN * 2, kLoads = S::BN / 32, kUnits = S::BN / 8;
+  static_assert(2 * kBuf + 4 * kList * 4 <= S::kLds, "two stages and each wave's entries");
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / S::WC, wc = wave % S::WC;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+  uint32_t* own = reinterpret_cast<uint32_t*>(smem + 2 * kBuf) + kList * wave;
+  // lane l's entry of the stage at e (past the list's end: its last, with nothing to add)
+  auto entry_at = [&](int e) { return g.order[min(e + lane, to - 1)]; };
+  auto rest_at = [&](int entry, int e) { return e + lane < to ? g.rest[entry >> 8] : 0.0f; };
+  auto issue = [&](int entry, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int r = 64 / kUnits * (kLoads * wave + q) + lane / kUnits;
+      const int t = __shfl(entry, r) >> 8;
+      const int col = min(8 * ((lane % kUnits) ^ (4 * (r & 3))), g.N - n0 - 8);
+      dma16(g.x + static_cast<size_t>(t) * g.N + n0 + col,
+            __builtin_amdgcn_readfirstlane(lds0 + buf * kBuf + (kLoads * wave + q) * 1024));
+    }
+  };
+  int entry = entry_at(from), next = entry_at(from + kList), buf = 0;
+  issue(entry, 0);
+  float rest = rest_at(entry, from);
+  for (int e = from; e < to; e += kList, buf ^= 1) {
+    own[lane] = static_cast<uint32_t>(entry & (S::BM - 1)) << 16 | f32_to_bf16(rest);
+    // the stage has landed, and every wave has read the one before
+    __builtin_amdgcn_s_waitcnt(nt_lgkm_only(0));
+    __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (e + kList < to) {
+      entry = next;
+      issue(entry, buf ^ 1);
+      rest = rest_at(entry, e + kList);
+      next = entry_at(e + 2 * kList);
+    }
+#pragma unroll
+    for (int s = 0; s < kList / 16; ++s) {
+      u32x4 x[S::NB];
+#pragma unroll
+      for (int n = 0; n < S::NB; ++n)
+        x[n] = nt_read_step(lds0 + buf * kBuf + nt_tr_at(lane, S::NB * wc + n, kUnits), S::BN * 2, s);
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = own[16 * s + 8 * (lane >> 5) + j];
+#pragma unroll
+      for (int m = 0; m < S::MB; ++m) {
+        const uint32_t col = 32 * (S::MB * wr + m) + (lane & 31);
+        u32x4 r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          r[j] = (w[2 * j] >> 16 == col ? w[2 * j] & 0xffffu : 0u) | (w[2 * j + 1] >> 16 == col ? w[2 * j + 1] << 16 : 0u);
+#pragma unroll
+        for (int n = 0; n < S::NB; ++n)
+          acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x[n]), __builtin_bit_cast(bf16x8, r),
+                                                              acc[m][n], 0, 0, 0);
+      }
+    }
+  }
+  __syncthreads();                                            // (the waves' stores go through the buffers)
+}
+
 template <class S, bool DW, bool SUMS>
 __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_product_kernel(ProductArgs g) {
   __shared__ __attribute__((aligned(1024))) unsigned char smem[S::kLds];
-  const int tiles = g.tiles_m * g.tiles_n;
-  const int z = blockIdx.x / tiles;
-  int tm, tn;
-  nt_tile(blockIdx.x - z * tiles, g.tiles_m, g.tiles_n, tm, tn);
+  int tm, tn, z;
+  nt_tile(blockIdx.x, g.tiles_m, g.tiles_n, g.parts, tm, tn, z);
   const int nk = g.K / kNtBK;
   const int k0 = static_cast<int>(static_cast<int64_t>(nk) * z / g.parts), k1 = static_cast<int>(static_cast<int64_t>(nk) * (z + 1) / g.parts);
   const int m0 = tm * S::BM, n0 = tn * S::BN;
@@ -287,8 +357,8 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
   const int wr = wave / S::WC, wc = wave % S::WC;
   const int mw = m0 + 32 * S::MB * wr, nw = n0 + 32 * S::NB * wc;
 
-  // What the targets' entries of P lost, read ahead of the reduction.  DW: the tile's
-  // list of rows with a target among its columns, 16 at a time as 16 more values of
+  // What the targets' entries of P lost, read ahead of the reduction.  DW: the first 16
+  // of the tile's list of rows with a target among its columns, as 16 more values of
   // the reduction, in bf16 (a target's entry then has 16 bits).
   struct Lost {
     int row[8];             // the column of P in the tile, -1: none
@@ -298,13 +368,13 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
   int list_at = 0, list_end = 0;
   // (scalar loads: a vector load's wait would count the stages under way)
   typedef const __attribute__((address_space(4))) int32_t* Scalars;
-  auto load_lost = [&](int e) __attribute__((always_inline)) {
+  auto load_lost = [&]() __attribute__((always_inline)) {
     int entries[16];                                       // (past the list's end: still in the workspace)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) entries[i] = ((Scalars)(g.order))[e + i];
+    for (int i = 0; i < 16; ++i) entries[i] = ((Scalars)(g.order))[list_at + i];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = e + 8 * (lane >> 5) + j;
+      const int i = list_at + 8 * (lane >> 5) + j;
       const int entry = i < list_end ? (lane < 32 ? entries[j] : entries[8 + j]) : -1;
       const int t = entry < 0 ? 0 : entry >> 8;
       lost.row[j] = entry < 0 ? -1 : entry & (S::BM - 1);
@@ -325,7 +395,7 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
       const int first = (g.v0 + m0) / kOrderCols;
       list_at = ((Scalars)(g.order_at))[first];
       list_end = ((Scalars)(g.order_at))[min(first + S::BM / kOrderCols, g.order_groups)];
-      if (list_at < list_end) load_lost(list_at);
+      if (list_at < list_end) load_lost();
     } else {
 #pragma unroll
       for (int m = 0; m < S::MB; ++m) {
@@ -337,7 +407,7 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
     }
   });
   if constexpr (DW) {
-    for (int e = list_at; e < list_end;) {
+    if (list_at < list_end) {
       bf16x8 r[S::MB];
 #pragma unroll
       for (int m = 0; m < S::MB; ++m)
@@ -350,8 +420,7 @@ __global__ __launch_bounds__(kNtThreads, S::kLds > 80 * 1024 ? 1 : 2) void head_
 #pragma unroll
         for (int n = 0; n < S::NB; ++n)
           acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lost.x[n], r[m], acc[m][n], 0, 0, 0);
-      e += 16;
-      if (e < list_end) load_lost(e);
+      if (list_at + 16 < list_end) add_listed<S>(g, list_at + 16, list_end, n0, smem, acc);
     }
   } else if (z == 0) {
     // row t takes rest[t] times its target's row of W
@@ -432,6 +501,7 @@ __global__ __launch_bounds__(256) void head_round_kernel(ProductArgs g) {
   if (row >= g.M || col >= g.N) return;
   const float4* sums = reinterpret_cast<const float4*>(g.sums);
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8                                            // (few waves: loads ahead of their additions, 7.0 us for 9.1)
   for (int z = 0; z < g.parts; ++z) {
     const float4 o = sums[sums_at<S>(z * g.tiles_m * g.tiles_n + tile, wave) + (block * 4 + q) * 64 + lane];
     v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
@@ -444,11 +514,11 @@ __global__ __launch_bounds__(256) void head_round_kernel(ProductArgs g) {
 // order[i] = row << 8 | target mod 256, order_at[g] the first of group g.  A workgroup
 // a group: the targets of lower groups give its place, then each wave writes the
 // matches of its quarter of the batch.
-__global__ __launch_bounds__(256) void head_order_kernel(const int32_t* target, int T, int V, int32_t* order,
-                                                         int32_t* order_at) {
+__device__ __forceinline__ void order_rows(int group, const int32_t* target, int T, int V, int32_t* order,
+                                           int32_t* order_at) {
   __shared__ int less_of[4], own_of[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int group = blockIdx.x, v0 = group * kOrderCols, v1 = min(v0 + kOrderCols, V);
+  const int v0 = group * kOrderCols, v1 = min(v0 + kOrderCols, V);
   const int quarter = (T + 255) / 256 * 64;
   const int from = wave * quarter, to = min(from + quarter, T);
   int less = 0, own = 0;
@@ -492,18 +562,18 @@ __global__ __launch_bounds__(256) void head_order_kernel(const int32_t* target, 
 // dst [cols, ldd] = src [rows, cols]^T in 64 x 64 tiles; columns of dst from rows to
 // ldd (a multiple of 64) are zero, and so are those of rows whose target is outside
 // the vocabulary (what stands in them may be no number)
-__global__ __launch_bounds__(256) void head_transpose_kernel(const bf16_t* src, int rows, int cols, bf16_t* dst, int ldd,
-                                                             const int32_t* target, int V) {
+__device__ __forceinline__ void transpose_rows(int block, const bf16_t* src, int rows, int cols, bf16_t* dst, int ldd,
+                                               const int32_t* target, int V) {
   __shared__ __attribute__((aligned(16))) bf16_t tile[64][72];
   const int tid = threadIdx.x;
   const int tr = ldd / 64;
-  const int r0 = static_cast<int>(blockIdx.x) % tr * 64, c0 = static_cast<int>(blockIdx.x) / tr * 64;
+  const int r0 = block % tr * 64, c0 = block / tr * 64;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 32 * i + tid / 8, c = tid % 8 * 8;
     u32x4 v = {0u, 0u, 0u, 0u};
     bool takes = r0 + r < rows && c0 + c < cols;
-    if (takes && target) {
+    if (takes) {
       const int y = target[r0 + r];
       takes = y >= 0 && y < V;
     }
@@ -525,6 +595,15 @@ __global__ __launch_bounds__(256) void head_transpose_kernel(const bf16_t* src, 
   }
 }
 
+// what dW's products need of the batch, in one launch
+__global__ __launch_bounds__(256) void head_prepare_kernel(const bf16_t* x, const int32_t* target, int T, int D, int V,
+                                                           int order_groups, int32_t* order, int32_t* order_at,
+                                                           bf16_t* xt, int ldt) {
+  const int b = blockIdx.x;
+  if (b < order_groups) order_rows(b, target, T, V, order, order_at);
+  else transpose_rows(b - order_groups, x, T, D, xt, ldt, target, V);
+}
+
 __global__ __launch_bounds__(256) void head_zero_kernel(u32x4* out, int64_t n) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
        i += static_cast<int64_t>(gridDim.x) * 256)
@@ -538,8 +617,8 @@ unsigned blocks_for(int64_t items) {
   return static_cast<unsigned>(want < 4096 ? want : 4096);
 }
 
-// What a backward pass holds: P and its transpose for a piece of the vocabulary of
-// about 2^27 entries (268 MB each; whole tiles; at least 8192 columns, under which
+// What a backward pass holds: P for a piece of the vocabulary of
+// about 2^27 entries (268 MB; whole tiles; at least 8192 columns, under which
 // dx's fp32 sums, read and written once a piece, would cost a third of its product),
 // x transposed, dx's sums.
 struct Plan {
@@ -723,8 +802,9 @@ hipError_t launch_head_loss_backward(int rows, int cols, int vocab, const bf16_t
   int32_t* order_at = reinterpret_cast<int32_t*>(ws + q.order_at);
   const int order_groups = (vocab + kOrderCols - 1) / kOrderCols;
   const int col_tiles = (cols + 63) / 64;
-  if (dw) head_order_kernel<<<order_groups, 256, 0, st>>>(target, rows, vocab, order, order_at);
-  if (dw) head_transpose_kernel<<<col_tiles * (q.ldt / 64), 256, 0, st>>>(x, rows, cols, xt, q.ldt, target, vocab);
+  if (dw)
+    head_prepare_kernel<<<order_groups + col_tiles * (q.ldt / 64), 256, 0, st>>>(x, target, rows, cols, vocab, order_groups,
+                                                                                order, order_at, xt, q.ldt);
   for (int v0 = 0; v0 < vocab; v0 += q.piece) {
     const int v1 = vocab - v0 < q.piece ? vocab : v0 + q.piece;
     const int ldp = up(v1 - v0, 64);

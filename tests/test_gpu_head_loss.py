@@ -388,3 +388,20 @@ def test_a_larger_batch_s_workspace():
     c.backward()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, c.guards))
+
+
+@pytest.mark.parametrize("rows,cols,vocab", [(97, 264, 40), (1500, 200, 300), (900, 1000, 513), (1024, 4096, 4096)])
+def test_a_few_targets_for_most_rows(rows, cols, vocab):
+    """lists of targets longer than one stage of the reduction, in both tiles' columns"""
+    c = Case(rows, cols, vocab, seed=21)
+    rng = np.random.default_rng(22)
+    few = rng.choice(vocab, 5, replace=False)
+    y = c.y.cpu().numpy()
+    often = rng.random(rows) < 0.85
+    y[often] = few[rng.integers(0, 5, int(often.sum()))]
+    c.y = torch.from_numpy(y).cuda()
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+    c.check_bands()
