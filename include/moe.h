@@ -312,8 +312,10 @@ int moe_grouped_down_fp8(const moe_shape* shape, const void* h, const int32_t* o
  *     to bf16 (1 where that gives zero); code = w / scale (fp32 quotient) to the
  *     nearest integer, ties to even, clamped to -8..7.
  * Activations stay bf16 (shape dtype MOE_BF16; anything else returns
- * MOE_ERR_UNSUPPORTED).  Weights must be finite (non-finite inputs give
- * unspecified codes); scales may be any bf16 value. */
+ * MOE_ERR_UNSUPPORTED), of magnitudes below 2^113: codes are stored with an offset
+ * of 8 that passes through the sums, so a row that holds a larger one or an infinity
+ * comes out as NaN (other rows are not touched by it).  Weights must be finite
+ * (non-finite inputs give unspecified codes); scales may be any bf16 value. */
 
 /* Bytes of `count` 4-bit [rows, cols] matrices (count * rows * cols / 2); 0 unless
  * rows is a multiple of 16 and cols of 128. */
@@ -630,9 +632,10 @@ int moe_head_loss_forward(int64_t rows, int32_t cols, int32_t vocab, int32_t dty
  *   workspace as for the forward pass
  * The vocabulary goes by in pieces, each piece's logits computed again.  P is
  * rounded to bf16 for the two products (the target's entry is held in more), dx and
- * dw once more.  All sums run in a fixed order: the results are bit-reproducible.  rows == 0 writes zeros to dw.
- * Outputs must not overlap the other arguments.  The workspace holds nothing between
- * calls; calls and captured graphs that may run at the same time need one each. */
+ * dw once more.  All sums run in a fixed order: the results are bit-reproducible.
+ * rows == 0 writes zeros to dw.  Outputs must not overlap the other arguments.  The
+ * workspace holds nothing between calls; calls and captured graphs that may run at the
+ * same time need one each. */
 int moe_head_loss_backward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,
                            const int32_t* target, const float* lse, const float* dloss, void* dx, void* dw,
                            void* workspace, size_t workspace_bytes, void* stream);

@@ -380,11 +380,14 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Arg
 // wave 64 of the weight rows (as above) and all 128 rows.  The rows' columns come
 // 128 at a time by direct global->LDS loads into two buffers, whole lines, the
 // 16-byte pieces of row r XOR-swizzled by r mod 16; weights go straight into
-// registers two stages ahead and are widened once for the 8 token blocks.  At most
+// registers half a stage ahead and are widened once for the 8 token blocks.  At most
 // 64 columns are summed before the scales: 32 operand registers a wave, so that two
 // workgroups share a CU and one's conversions run beside the other's MFMAs.
 // Tiles in order of expert, column tile, row block, each XCD a run of them, so that
-// an expert's rows and a column tile's weights stay behind one L2.
+// an expert's rows and a column tile's weights stay behind one L2.  An expert's rows
+// are split evenly, and each number of token blocks has its own loop: 4500 tokens of
+// 8 experts each down K = 1024 in 515 us with blocks of 128 rows and a rest and every
+// second number, 492 split evenly, 473 with each number.
 template <int MODE, int G>
 __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
   constexpr int NB = 4, TB = 8, kRows = 16 * TB;
@@ -419,9 +422,9 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
   if (in_xcd >= share + (xcd < rem ? 1 : 0)) return;
   int t = xcd * share + min(xcd, rem) + in_xcd;
   const bool shared = t < n_s;
-  int e = 0, lo = 0, M = a.T, tile, m0;
+  int e = 0, lo = 0, M = a.T, tile, chunk, chunks = chunks_s;
   if (shared) {
-    m0 = t % chunks_s * kRows;
+    chunk = t % chunks_s;
     tile = t / chunks_s;
   } else {
     t -= n_s;
@@ -442,16 +445,18 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
     lo = __builtin_amdgcn_readlane(from, src);
     M = __builtin_amdgcn_readlane(to, src) - lo;
     const int local = t - __builtin_amdgcn_readlane(first, src) * a.tiles_r;
-    const int chunks = (M + kRows - 1) / kRows;
-    m0 = local % chunks * kRows;
+    chunks = (M + kRows - 1) / kRows;
+    chunk = local % chunks;
     tile = local / chunks;
   }
+  // as even row blocks as whole token blocks allow (none is empty: M > 128 (chunks - 1))
+  const int size = (M + 16 * chunks - 1) / (16 * chunks) * 16, m0 = chunk * size;
   const int K = shared ? a.Ks : a.K;
   const int N = shared ? a.Ns : a.N;
   const int Nw = MODE == kInt4GateUp ? 2 * N : N;
   const int ncb = K / kColBlock;
   const int n0 = (tile * 4 + wave) * kCols;
-  const int valid = min(kRows, M - m0);
+  const int valid = min(size, M - m0);
   const int tbv = (valid + 15) / 16;                      // token blocks with rows
 
   // ---- sources
@@ -575,9 +580,12 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
       compute(f, cb, nt_tag);
     }
   };
-  if (tbv > 6) k_loop(std::integral_constant<int, 8>{});
-  else if (tbv > 4) k_loop(std::integral_constant<int, 6>{});
-  else if (tbv > 2) k_loop(std::integral_constant<int, 4>{});
+  if (tbv > 7) k_loop(std::integral_constant<int, 8>{});
+  else if (tbv > 6) k_loop(std::integral_constant<int, 7>{});
+  else if (tbv > 5) k_loop(std::integral_constant<int, 6>{});
+  else if (tbv > 4) k_loop(std::integral_constant<int, 5>{});
+  else if (tbv > 3) k_loop(std::integral_constant<int, 4>{});
+  else if (tbv > 2) k_loop(std::integral_constant<int, 3>{});
   else k_loop(std::integral_constant<int, 2>{});
 
   // ---- out through LDS: [row][the tile's columns], pieces of 16 bytes swizzled

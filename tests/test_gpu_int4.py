@@ -348,3 +348,16 @@ def test_decode_workload():
     torch.cuda.synchronize()
     ref, _ = O.forward(I.Int4Weights(inp, 128), s.alpha, s.k, logits32=b.logits.cpu().numpy())
     assert_close_rel(to_f64(b.out), ref, out_tolerance(s), "out (4-bit weights)")
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("mode", ["gate_up", "down"])
+def test_row_blocks_of_every_size(mode, group):
+    """experts' rows around whole row blocks, and each number of token blocks in one"""
+    say(f"int4 {mode} row blocks, group {group}")
+    counts = [1, 17, 33, 49, 65, 81, 97, 113, 128, 129, 145, 177, 209, 256, 257, 289, 385]
+    T = sum(counts) + 3
+    c = Case(mode, T, 256, 256, 256, group, counts, 1, seed=31)
+    c.run()
+    torch.cuda.synchronize()
+    c.check()
