@@ -80,6 +80,14 @@ __device__ __forceinline__ u32x4 load16(const void* base, uint32_t off) {
   else return *p;
 }
 
+// Between LDS writes of some of a wave's lanes and reads of others, both ways: the
+// hardware does a wave's LDS operations in order, and the compiler, which sees one lane
+// at a time, moves none across.  No instruction.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // One workgroup: a column tile of one expert, its rows up to 16 TM at a time.  Four
 // waves of 64 weight rows each (gate_up: 32 gate rows and the up rows of the same
 // columns): ks of them share the reduction, 4 / ks stand side by side.  Weights go
@@ -250,8 +258,8 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Arg
     auto compute = [&](const u32x4 (&wq)[NB], int j, bool odd) __attribute__((always_inline)) {   // block j of the run
       constexpr int SG = 4 / GC;                         // MFMA steps of a group
       const u32x4 offset = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};   // -136
-      // (a wave's LDS operations are done in order; tokens past 4 NI - 1 hold what
-      // was there, and only outputs that are not stored depend on them)
+      // (tokens past 4 NI - 1 hold what was there, and only outputs that are not
+      // stored depend on them)
       bf16x8 x[TB][4];
 #pragma unroll
       for (int t = 0; t < TB; ++t)
@@ -324,8 +332,10 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Arg
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
           keep_rows();
+          wave_lds_fence();
           load_rows(cb + q + 1);
           if (cb + q < c1) compute(ring[q], (cb - c0) % kRun + q, q % 2 != 0);
+          wave_lds_fence();
           load(ring[q], cb + q + kAhead);
         }
       }
