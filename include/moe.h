@@ -312,10 +312,10 @@ int moe_grouped_down_fp8(const moe_shape* shape, const void* h, const int32_t* o
  *     to bf16 (1 where that gives zero); code = w / scale (fp32 quotient) to the
  *     nearest integer, ties to even, clamped to -8..7.
  * Activations stay bf16 (shape dtype MOE_BF16; anything else returns
- * MOE_ERR_UNSUPPORTED), of magnitudes below 2^113: codes are stored with an offset
- * of 8 that passes through the sums, so a row that holds a larger one or an infinity
- * comes out as NaN (other rows are not touched by it).  Weights must be finite
- * (non-finite inputs give unspecified codes); scales may be any bf16 value. */
+ * MOE_ERR_UNSUPPORTED).  A code of 0 adds exactly nothing for any finite activation;
+ * a row that holds an infinity or NaN comes out without finite values (0 times
+ * infinity is NaN) and touches no other.  Weights must be finite (non-finite inputs
+ * give unspecified codes); scales may be any bf16 value. */
 
 /* Bytes of `count` 4-bit [rows, cols] matrices (count * rows * cols / 2); 0 unless
  * rows is a multiple of 16 and cols of 128. */

@@ -8,19 +8,18 @@
 //   gate_up  h[p] = silu(y_gate) * y_up;   down  y[p]
 // for the rows p of each expert, and for the shared expert over all tokens.
 //
-// Numbers.  A code is stored as q + 8; 128 + (q + 8) is a bf16 whose low mantissa
-// bits are the code, so eight codes become an MFMA operand with four AND-ORs and
-// three shifts, no conversion.  The offset leaves again through the accumulator:
-// a group's MFMA chain starts from -136 sum_{c in g} a[p, c], itself an MFMA
-// chain with a constant operand, shared by all weight rows of the wave.  The
-// products are exact, the sums fp32; the offset makes their rounding about 30
-// times that of a plain fp32 sum (2e-6 of a group's result, against 2^-8 of the
-// bf16 output).  A group's sum is then multiplied by its scale in fp32.
+// Numbers.  A code is stored as q + 8 and widened to q in bf16, exactly (widen), so
+// that products are exact and sums are fp32 sums of the terms themselves: a code of 0
+// adds nothing, whatever its activation.  (128 + code would be one AND-OR for two
+// codes, but its offset has to leave again through the sum and leaves a rounding of
+// 136 sum |a|: 5e-4 instead of 0 for weights of zero under unit activations with
+// outliers of 50, and a fifth more MFMAs.  Exact codes cost decode 4%, 32 tokens at the
+// M.1 widths 67 -> 69 us, and one token 12.7 -> 14.8 us; long prompts gain 5%.)  A group's
+// sum is then multiplied by its scale in fp32.
 //
 // Layout.  Blocks of 16 rows x 128 columns, 1 KB, row-block major: lane l's 16
 // bytes are its codes of four 16x16x32 MFMA steps, row l mod 16, columns
-// 32 i + 8 (l / 16) .. + 7 of dword i, element e in nibble e / 2 + 4 (e mod 2)
-// (so that one mask takes out elements 2j and 2j + 1 as a bf16 pair).
+// 32 i + 8 (l / 16) .. + 7 of dword i, element e in nibble e / 2 + 4 (e mod 2).
 #include "int4.h"
 
 #include <type_traits>
@@ -54,20 +53,41 @@ struct Int4Args {
   int ks_r, ks_s;            // waves of a workgroup that share a tile's reduction
 };
 
-// The constants of widen, one in a scalar and one in a vector register: an AND-OR
-// takes one of each, and with literals the compiler emits an AND and an OR.
-struct Widen {
-  uint32_t mask, base;
-  __device__ __forceinline__ Widen() : mask(0x000f000fu), base(0x43004300u) {
-    asm volatile("" : "+s"(mask));
-    asm volatile("" : "+v"(base));
+// Eight codes q + 8 -> q in bf16.  gfx950 converts two E4M3 bytes at a time, and a byte up
+// to 15 counts 2^-9 there (8 and up are the lowest normal binade): so magnitudes and signs
+// of all eight in their nibbles first, then in bytes, the even nibbles' and the odd ones'.
+// Those are elements 0 4 1 5 and 2 6 3 7; unless IN_ORDER the operand keeps that order, and
+// the activations take it too (reorder).  12 instructions, 14 in order.
+template <bool IN_ORDER>
+__device__ __forceinline__ bf16x8 widen(uint32_t w) {
+  // (as three-operand logic: written out, the compiler makes more of it)
+  auto and_not = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_bitop3_b32(a, b, b, 0x30); };   // a & ~b
+  auto choose = [](uint32_t a, uint32_t m, uint32_t b) { return __builtin_amdgcn_bitop3_b32(a, m, b, 0xe2); };   // m ? a : b
+  const uint32_t low = 0x0f0f0f0fu;
+  const uint32_t minus = and_not(0x88888888u, w), one = minus >> 3;
+  const uint32_t mag = (w ^ (0x88888888u - one)) + one;    // code below 8: 7 - code + 1; else code - 8
+  uint32_t even = choose(mag, low, minus << 4), odd = choose(mag >> 4, low, minus);
+  if constexpr (IN_ORDER) {
+    even = __builtin_amdgcn_perm(even, even, 0x03010200u);
+    odd = __builtin_amdgcn_perm(odd, odd, 0x03010200u);
   }
-  // eight codes -> the bf16 operand 128 + code (element e from nibble e / 2 + 4 (e mod 2))
-  __device__ __forceinline__ bf16x8 operator()(uint32_t w) const {
-    const u32x4 v = {(w & mask) | base, ((w >> 4) & mask) | base, ((w >> 8) & mask) | base, ((w >> 12) & mask) | base};
-    return __builtin_bit_cast(bf16x8, v);
-  }
-};
+  auto pair = [](uint32_t v, auto high) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.0f, decltype(high)::value));
+  };
+  const std::false_type lo{};
+  const std::true_type hi{};
+  // in order: elements 0 1 4 5 | 2 3 6 7
+  const u32x4 v = IN_ORDER ? u32x4{pair(even, lo), pair(odd, lo), pair(even, hi), pair(odd, hi)}
+                           : u32x4{pair(even, lo), pair(even, hi), pair(odd, lo), pair(odd, hi)};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// eight activations in the order of widen<false>'s elements
+__device__ __forceinline__ u32x4 reorder(const u32x4& x) {
+  auto lows = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); };
+  auto highs = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };
+  return u32x4{lows(x[0], x[2]), highs(x[0], x[2]), lows(x[1], x[3]), highs(x[1], x[3])};
+}
 
 // 16 bytes at a base that is the same in every lane plus the lane's own offset.
 // The offset is made opaque where it is used: otherwise the compiler adds the two
@@ -232,7 +252,6 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Arg
       const int row = min(4 * i + (lane >> 4), M - 1 - m0);
       tok[i] = !shared && a.gather ? a.gather[lo + m0 + row] : row;
     }
-    const Widen widen;
     f32x4 acc[TB][NB];
 #pragma unroll
     for (int t = 0; t < TB; ++t)
@@ -252,12 +271,11 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Arg
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int r = 4 * i + (lane >> 4);
-        *reinterpret_cast<u32x4*>(my_rows + r * 256 + (((lane & 15) ^ (r & 15)) << 4)) = rows[i];
+        *reinterpret_cast<u32x4*>(my_rows + r * 256 + (((lane & 15) ^ (r & 15)) << 4)) = reorder(rows[i]);
       }
     };
     auto compute = [&](const u32x4 (&wq)[NB], int j, bool odd) __attribute__((always_inline)) {   // block j of the run
       constexpr int SG = 4 / GC;                         // MFMA steps of a group
-      const u32x4 offset = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};   // -136
       // (tokens past 4 NI - 1 hold what was there, and only outputs that are not
       // stored depend on them)
       bf16x8 x[TB][4];
@@ -279,25 +297,17 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Arg
         const auto p23 = __builtin_amdgcn_permlane16_swap(p[1], p[1], false, false);
         const float sc[NB] = {__uint_as_float(p01[0]), __uint_as_float(p01[1]), __uint_as_float(p23[0]),
                               __uint_as_float(p23[1])};
-        f32x4 start[TB];
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-          start[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < SG; ++i)
-            start[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][g * SG + i], __builtin_bit_cast(bf16x8, offset),
-                                                                start[t], 0, 0, 0);
-        }
         // a step of all blocks at a time: NB TB chains side by side
         f32x4 y[TB][NB];
 #pragma unroll
         for (int i = 0; i < SG; ++i) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const bf16x8 w = widen(wq[b][g * SG + i]);
+            const bf16x8 w = widen<false>(wq[b][g * SG + i]);
 #pragma unroll
             for (int t = 0; t < TB; ++t)
-              y[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][g * SG + i], w, i == 0 ? start[t] : y[t][b], 0, 0, 0);
+              y[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[t][g * SG + i], w, i == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : y[t][b],
+                                                                0, 0, 0);
           }
           __builtin_amdgcn_sched_barrier(0);              // a step's operands at a time
         }
@@ -395,9 +405,10 @@ __global__ __launch_bounds__(256, TM == 1 ? 3 : 2) void int4_rows_kernel(Int4Arg
 // workgroups share a CU and one's conversions run beside the other's MFMAs.
 // Tiles in order of expert, column tile, row block, each XCD a run of them, so that
 // an expert's rows and a column tile's weights stay behind one L2.  An expert's rows
-// are split evenly, and each number of token blocks has its own loop: 4500 tokens of
-// 8 experts each down K = 1024 in 515 us with blocks of 128 rows and a rest and every
-// second number, 492 split evenly, 473 with each number.
+// are split evenly, and each number of token blocks has its own loop: 4096 tokens at
+// D = 4096, F = 1024 (128 rows an expert) gate/up 705 us, 755 with blocks of 128 rows and
+// a rest and every second number, 778 split evenly with every second number; down 396, 418
+// and 407.
 template <int MODE, int G>
 __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
   constexpr int NB = 4, TB = 8, kRows = 16 * TB;
@@ -516,7 +527,6 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
       for (int g = 0; g < GC / 2; ++g) f.s[g] = reinterpret_cast<const uint32_t*>(from)[g];
     }
   };
-  const Widen widen;
   f32x4 acc[TB][NB];
 #pragma unroll
   for (int i = 0; i < TB; ++i)
@@ -526,7 +536,6 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
   auto compute = [&](Stage& f, int cb, auto nt_tag) __attribute__((always_inline)) {
     constexpr int NT = decltype(nt_tag)::value;
     const unsigned char* X = smem + (cb & 1) * kStage;
-    const u32x4 offset = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};   // -136
     constexpr int SG = G == 32 ? 1 : 2;                   // MFMA steps before the scales
 #pragma unroll
     for (int part = 0; part < 4 / SG; ++part) {
@@ -542,7 +551,7 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
 #pragma unroll
       for (int i = 0; i < SG; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) w[i][b] = widen(f.w[b][part * SG + i]);
+        for (int b = 0; b < NB; ++b) w[i][b] = widen<true>(f.w[b][part * SG + i]);
       // (the registers of the packed weights are free: the next stage's)
       if (part == 4 / SG - 1) load(f, cb + 1);
       auto read = [&](bf16x8 (&x)[SG], int i) __attribute__((always_inline)) {
@@ -558,15 +567,12 @@ __global__ __launch_bounds__(256, 2) void int4_tile_kernel(Int4Args a) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         if (i + 1 < NT) read(x[(i + 1) & 1], i + 1);
-        f32x4 start = {0.f, 0.f, 0.f, 0.f}, y[NB];
-#pragma unroll
-        for (int k = 0; k < SG; ++k)
-          start = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][k], __builtin_bit_cast(bf16x8, offset), start, 0, 0, 0);
+        f32x4 y[NB];
 #pragma unroll
         for (int k = 0; k < SG; ++k)
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            y[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][k], w[k][b], k == 0 ? start : y[b], 0, 0, 0);
+            y[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i & 1][k], w[k][b], k == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : y[b], 0, 0, 0);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -701,8 +707,9 @@ hipError_t launch_rows(Int4Args a, int group, hipStream_t st) {
   // Waves that share a reduction.  More of them make more workgroups of the same
   // rows, which evens out their last round; each costs a start (offsets, row ids,
   // first loads: 4 to 6 us, beside the others').  So up to 4096 workgroups as long
-  // as a wave keeps 8 blocks (32 tokens, D = 4096, F = 1024: gate/up 64 us split in
-  // 2, 69 whole; down, K = 1024, 38 split, 36 whole), and up to 1024 at any length.
+  // as a wave keeps 8 blocks, and up to 1024 at any length (D = 4096, F = 1024, even
+  // popularity: 32 tokens' gate/up 118 us, 130 whole, 125 in fours; 1 token's 14.5, 30
+  // whole; 32 tokens' down, K = 1024, 66, 66 and 86).
   auto split = [&](int K, int N, int64_t chunks) {
     int ks = 1;
     for (; ks < 4; ks *= 2) {
@@ -748,14 +755,16 @@ template <int MODE>
 hipError_t launch_int4(const Int4Args& a, int group, hipStream_t st) {
   // By the mean rows an expert.  The tile kernel spreads a weight's conversion over
   // 128 rows but streams weights more slowly; scales of 32 columns cost it more.
-  // Measured at D = 4096, F = 1024 (groups of 128, us, rows kernel and tile kernel):
-  // gate/up 242, 304 at 16 rows, 299, 326 at 24, 385, 358 at 32; down (K = 1024) 139,
-  // 151 at 12, 165, 160 at 16, 193, 173 at 24; groups of 32: gate/up 433, 464 at 32,
-  // down 184, 200 at 16, 222, 212 at 24.
+  // Measured at D = 4096, F = 1024 (us: 16-row, 32-row and tile kernel), groups of 128:
+  // gate/up 230, 245, 301 at 12 rows, 259, 252, 316 at 14, 405, 315, 323 at 24, 454, 356,
+  // 328 at 28; down (K = 1024) 138, 148, 164 at 12, 150, 157, 165 at 14, 169, 166, 168 at
+  // 16, 186, 171, 167 at 18; groups of 32: gate/up 504, 405, 424 at 28, 560, 470, 441 at
+  // 32, down 224, 201, 203 at 20, 248, 217, 208 at 24.  The shared expert's T rows go
+  // with the routed ones.
   const int mean = a.S / a.E;
-  const int tiles_from = MODE == kInt4GateUp ? (group == 32 ? 40 : 28) : (group == 32 ? 20 : 14);
+  const int tiles_from = MODE == kInt4GateUp ? (group == 32 ? 30 : 26) : (group == 32 ? 22 : 17);
   if (mean >= tiles_from) return launch_tiles4<MODE>(a, group, st);
-  if (mean >= 12) return launch_rows<MODE, 2>(a, group, st);
+  if (mean >= 14) return launch_rows<MODE, 2>(a, group, st);
   return launch_rows<MODE, 1>(a, group, st);
 }
 
