@@ -629,6 +629,7 @@ int moe_head_loss_forward(int64_t rows, int32_t cols, int32_t vocab, int32_t dty
  *           mean over N rows)
  *   dx      [rows, cols] bf16 out;  dw [vocab, cols] bf16 out; either may be NULL
  *           (not computed), not both
+ *           (rows == 0: dw alone counts, and may be NULL too)
  *   workspace as for the forward pass
  * The vocabulary goes by in pieces, each piece's logits computed again.  P is
  * rounded to bf16 for the two products (the target's entry is held in more), dx and

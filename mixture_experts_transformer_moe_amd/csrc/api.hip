@@ -944,8 +944,8 @@ int moe_head_loss_backward(int64_t rows, int32_t cols, int32_t vocab, int32_t dt
   if (int r = check_head(rows, cols, vocab, dtype)) return r;
   OPT_PTR(dx);
   OPT_PTR(dw);
-  if (dx == nullptr && dw == nullptr) return fail(MOE_ERR_INVALID_ARG, "dx and dw are both NULL");
   if (rows > 0) {
+    if (dx == nullptr && dw == nullptr) return fail(MOE_ERR_INVALID_ARG, "dx and dw are both NULL");
     NEED_PTR(x);
     NEED_PTR(w);
     NEED_PTR(target);
