@@ -9,6 +9,7 @@ status raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Dict, Optional
@@ -319,17 +320,19 @@ def moe_int4_packed_bytes(count, rows, cols) -> int:
 
 
 def moe_quantize_weights_int4(w, w_int4, scales, count, rows, cols, group, stream=None):
-    dev, n = w.get_device(), int(count) * int(rows) * int(cols)
+    dev, bf = w.get_device(), torch.bfloat16
+    count, rows, cols, group = int(count), int(rows), int(cols), int(group)
     _check(lib().moe_quantize_weights_int4(
-        _flat(w, n, torch.bfloat16, dev, "w"), _flat(w_int4, n // 2, torch.uint8, dev, "w_int4"),
-        _flat(scales, n // group if group else 0, torch.bfloat16, dev, "scales"), int(count), int(rows), int(cols),
-        int(group), _stream_on(stream, dev)), "moe_quantize_weights_int4")
+        _flat(w, (count, rows, cols), bf, dev, "w"), _flat(w_int4, count * rows * cols // 2, torch.uint8, dev, "w_int4"),
+        _flat(scales, (count, rows, cols // (group or 1)), bf, dev, "scales"), count, rows, cols, group,
+        _stream_on(stream, dev)), "moe_quantize_weights_int4")
 
 
 def moe_pack_weights_int4(codes, w_int4, count, rows, cols, stream=None):
-    dev, n = codes.get_device(), int(count) * int(rows) * int(cols) // 2
-    _check(lib().moe_pack_weights_int4(_flat(codes, n, torch.uint8, dev, "codes"),
-                                       _flat(w_int4, n, torch.uint8, dev, "w_int4"), int(count), int(rows), int(cols),
+    dev, u8 = codes.get_device(), torch.uint8
+    count, rows, cols = int(count), int(rows), int(cols)
+    _check(lib().moe_pack_weights_int4(_flat(codes, (count, rows, cols // 2), u8, dev, "codes"),
+                                       _flat(w_int4, count * rows * cols // 2, u8, dev, "w_int4"), count, rows, cols,
                                        _stream_on(stream, dev)), "moe_pack_weights_int4")
 
 
@@ -365,14 +368,14 @@ def moe_grouped_gate_up_int4(shape, group, x_perm, sorted_token, x, offsets, w_g
                              ws_gate_up, ws_gate_up_scale, h, stream=None):
     dev, u8, bf, i32 = x.get_device(), torch.uint8, torch.bfloat16, torch.int32
     T, D, E, F, Fs, S = shape.T, shape.D, shape.E, shape.F, shape.Fs, shape.T * shape.k
-    n, ns, g = E * 2 * F * D, 2 * Fs * D, group or 1
+    g = group or 1
     _check(lib().moe_grouped_gate_up_int4(
-        ctypes.byref(shape), group, _flat(x_perm, S * D, bf, dev, "x_perm"),
-        _flat(sorted_token, S, i32, dev, "sorted_token") if x_perm is None else None, _flat(x, T * D, bf, dev, "x"),
-        _flat(offsets, E + 1, i32, dev, "offsets"), _flat(w_gate_up, n // 2, u8, dev, "w_gate_up"),
-        _flat(w_gate_up_scale, n // g, bf, dev, "w_gate_up_scale"),
-        _flat(ws_gate_up, ns // 2, u8, dev, "ws_gate_up") if Fs else None,
-        _flat(ws_gate_up_scale, ns // g, bf, dev, "ws_gate_up_scale") if Fs else None,
+        ctypes.byref(shape), group, _flat(x_perm, (S, D), bf, dev, "x_perm"),
+        _flat(sorted_token, (S,), i32, dev, "sorted_token") if x_perm is None else None, _flat(x, (T, D), bf, dev, "x"),
+        _flat(offsets, (E + 1,), i32, dev, "offsets"), _flat(w_gate_up, E * F * D, u8, dev, "w_gate_up"),
+        _flat(w_gate_up_scale, (E, 2 * F, D // g), bf, dev, "w_gate_up_scale"),
+        _flat(ws_gate_up, Fs * D, u8, dev, "ws_gate_up") if Fs else None,
+        _flat(ws_gate_up_scale, (2 * Fs, D // g), bf, dev, "ws_gate_up_scale") if Fs else None,
         _flat(h, S * F + T * Fs, bf, dev, "h"), _stream_on(stream, dev)), "moe_grouped_gate_up_int4")
 
 
@@ -380,13 +383,14 @@ def moe_grouped_down_int4(shape, group, h, offsets, w_down, w_down_scale, ws_dow
                           y_shared, stream=None):
     dev, u8, bf = h.get_device(), torch.uint8, torch.bfloat16
     T, D, E, F, Fs, S = shape.T, shape.D, shape.E, shape.F, shape.Fs, shape.T * shape.k
-    n, ns, g = E * D * F, D * Fs, group or 1
+    g = group or 1
     _check(lib().moe_grouped_down_int4(
         ctypes.byref(shape), group, _flat(h, S * F + T * Fs, bf, dev, "h"),
-        _flat(offsets, E + 1, torch.int32, dev, "offsets"), _flat(w_down, n // 2, u8, dev, "w_down"),
-        _flat(w_down_scale, n // g, bf, dev, "w_down_scale"), _flat(ws_down, ns // 2, u8, dev, "ws_down") if Fs else None,
-        _flat(ws_down_scale, ns // g, bf, dev, "ws_down_scale") if Fs else None,
-        _flat(y_perm, S * D, bf, dev, "y_perm"), _flat(y_shared, T * D, bf, dev, "y_shared") if Fs else None,
+        _flat(offsets, (E + 1,), torch.int32, dev, "offsets"), _flat(w_down, E * D * F // 2, u8, dev, "w_down"),
+        _flat(w_down_scale, (E, D, F // g), bf, dev, "w_down_scale"),
+        _flat(ws_down, D * Fs // 2, u8, dev, "ws_down") if Fs else None,
+        _flat(ws_down_scale, (D, Fs // g), bf, dev, "ws_down_scale") if Fs else None,
+        _flat(y_perm, (S, D), bf, dev, "y_perm"), _flat(y_shared, (T, D), bf, dev, "y_shared") if Fs else None,
         _stream_on(stream, dev)), "moe_grouped_down_int4")
 
 
@@ -767,16 +771,26 @@ def _arg(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Opt
     return t.data_ptr()
 
 
-def _flat(t: Optional[torch.Tensor], numel: int, dtype, device: int, what: str) -> Optional[int]:
-    """Address of an argument of numel elements in any shape (on CUDA device `device`), or None."""
+def _flat(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Optional[int]:
+    """Address of a row-major argument (on CUDA device `device`), or None: of `shape`, flat, or
+    with its leading dimensions joined; an int allows any shape of that many elements."""
     if t is None:
         return None
-    if t.numel() != numel or t.dtype is not dtype or t.get_device() != device:
-        raise ValueError(f"{what} has {t.numel()} elements of {t.dtype} on {t.device}: "
-                         f"{numel} of {dtype} on the device of the others are wanted")
+    if t.dtype is not dtype or t.get_device() != device or (t.shape != shape and not _same_order(t.shape, shape)):
+        raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype} on {t.device}: "
+                         f"{shape} {dtype} on the device of the others is wanted")
     if device < 0 or not t.is_contiguous():
         _ptr(t)                                        # (raises)
     return t.data_ptr()
+
+
+def _same_order(got, shape) -> bool:
+    if isinstance(shape, int):
+        return got.numel() == shape
+    while len(got) > 1 and got[0] == 1 and got != shape:
+        got = got[1:]
+    joined = len(shape) - len(got)                     # dimensions that the first one of `got` holds beside its own
+    return joined >= 0 and len(got) > 0 and got[0] == math.prod(shape[:joined + 1]) and got[1:] == shape[joined + 1:]
 
 
 def _workspace_arg(t: Optional[torch.Tensor], device: int) -> Optional[int]:

@@ -1,0 +1,20 @@
+"""Which shapes of a row-major argument hold its elements where the library reads them."""
+import pytest
+import torch
+
+from mixture_experts_transformer_moe_amd import binding as M
+
+
+@pytest.mark.parametrize("shape,good,bad", [
+    ((4, 6, 3), [(4, 6, 3), (24, 3), (72,), (1, 4, 6, 3)], [(4, 3, 6), (6, 4, 3), (4, 18), (3, 24), (4, 6, 3, 1), (2, 2, 6, 3)]),
+    ((6, 3), [(6, 3), (18,), (1, 6, 3), (1, 1, 6, 3)], [(3, 6), (6, 1, 3), (2, 3, 3), (9, 2)]),
+    ((5,), [(5,), (1, 5)], [(5, 1), (6,)]),
+    (7, [(7,), (1, 7), (7, 1)], [(8,)]),
+])
+def test_shapes(shape, good, bad):
+    for s in good:
+        with pytest.raises(ValueError, match="host|CUDA|cuda|device"):            # (the shape is right: it is a host tensor)
+            M._flat(torch.zeros(s), shape, torch.float32, -1, "scales")
+    for s in bad:
+        with pytest.raises(ValueError, match=r"scales is \("):
+            M._flat(torch.zeros(s), shape, torch.float32, -1, "scales")
