@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "grouped_gemm.h"
+#include "int4_plan.h"
 #include "mma_stream.h"
 
 namespace moe {
@@ -704,25 +705,10 @@ hipError_t launch_rows(Int4Args a, int group, hipStream_t st) {
   // chunks the experts' rows can make
   const int64_t most = static_cast<int64_t>(a.E) + a.S / kChunk;
   const int64_t slots = a.S < most ? a.S : most;
-  // Waves that share a reduction.  More of them make more workgroups of the same
-  // rows, which evens out their last round; each costs a start (offsets, row ids,
-  // first loads: 4 to 6 us, beside the others').  So up to 4096 workgroups as long
-  // as a wave keeps 8 blocks, and up to 1024 at any length (D = 4096, F = 1024, even
-  // popularity: 32 tokens' gate/up 118 us, 130 whole, 125 in fours; 1 token's 14.5, 30
-  // whole; 32 tokens' down, K = 1024, 66, 66 and 86).
-  auto split = [&](int K, int N, int64_t chunks) {
-    int ks = 1;
-    for (; ks < 4; ks *= 2) {
-      const int64_t groups = chunks * (N / (kCols * (4 / ks)));
-      const int blocks = K / kColBlock / (2 * ks);        // of a wave after one more split
-      if (!(blocks >= 8 && groups < 4096) && !(blocks >= 2 && groups < 1024)) break;
-    }
-    return ks;
-  };
-  a.ks_r = split(a.K, a.N, slots);
+  a.ks_r = int4_split(a.K / kColBlock, a.N, kCols, slots);
   a.tiles_r = a.N / (kCols * (4 / a.ks_r));
   const int64_t chunks_s = (a.T + kChunk - 1) / kChunk;
-  a.ks_s = a.Ns > 0 ? split(a.Ks, a.Ns, chunks_s) : 1;
+  a.ks_s = a.Ns > 0 ? int4_split(a.Ks / kColBlock, a.Ns, kCols, chunks_s) : 1;
   a.tiles_s = a.Ns > 0 ? a.Ns / (kCols * (4 / a.ks_s)) : 0;
   const int64_t grid = a.tiles_s * chunks_s + slots * a.tiles_r;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
@@ -753,19 +739,11 @@ hipError_t launch_tiles4(Int4Args a, int group, hipStream_t st) {
 
 template <int MODE>
 hipError_t launch_int4(const Int4Args& a, int group, hipStream_t st) {
-  // By the mean rows an expert.  The tile kernel spreads a weight's conversion over
-  // 128 rows but streams weights more slowly; scales of 32 columns cost it more.
-  // Measured at D = 4096, F = 1024 (us: 16-row, 32-row and tile kernel), groups of 128:
-  // gate/up 230, 245, 301 at 12 rows, 259, 252, 316 at 14, 405, 315, 323 at 24, 454, 356,
-  // 328 at 28; down (K = 1024) 138, 148, 164 at 12, 150, 157, 165 at 14, 169, 166, 168 at
-  // 16, 186, 171, 167 at 18; groups of 32: gate/up 504, 405, 424 at 28, 560, 470, 441 at
-  // 32, down 224, 201, 203 at 20, 248, 217, 208 at 24.  The shared expert's T rows go
-  // with the routed ones.
-  const int mean = a.S / a.E;
-  const int tiles_from = MODE == kInt4GateUp ? (group == 32 ? 30 : 26) : (group == 32 ? 22 : 17);
-  if (mean >= tiles_from) return launch_tiles4<MODE>(a, group, st);
-  if (mean >= 14) return launch_rows<MODE, 2>(a, group, st);
-  return launch_rows<MODE, 1>(a, group, st);
+  switch (int4_kernel(MODE == kInt4GateUp, group, a.S, a.E)) {
+    case Int4Kernel::kTiles: return launch_tiles4<MODE>(a, group, st);
+    case Int4Kernel::kRows32: return launch_rows<MODE, 2>(a, group, st);
+    default: return launch_rows<MODE, 1>(a, group, st);
+  }
 }
 
 int grid_for(int64_t items) {

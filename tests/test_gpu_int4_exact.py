@@ -19,7 +19,7 @@ from tests.test_gpu_int4 import b16, bf16, u32, Case
 pytestmark = pytest.mark.gpu
 
 # rows an expert in the kernel of 16 rows, of 32, and in the tile kernel (both directions)
-ROWS = [3, 12, 45]
+ROWS = [3, 15, 45]
 
 
 def groups_of(w, a, scales, group):
