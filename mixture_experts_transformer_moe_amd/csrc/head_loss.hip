@@ -13,12 +13,16 @@
 // is computed again, P leaves the accumulators once as bf16, and two products follow,
 // each with one operand read across its rows (gemm_nt.h): P W, and P^T with x
 // transposed once (rows without part as zeros).  dx is summed over pieces in fp32.
-// P in bf16 is the one rounding inside: 1.7e-3 of an entry, independent from entry
-// to entry.  The target's entry, p - 1 from fp32, is most of a row's norm, and its
-// rounding is common to all of the row: what it lost is kept in fp32 and added to
-// both products (333 x 1000 over 33001: 2.4e-3 of the gradients' norm without it, up
-// to 3.4e-3 for single rows, 1.66e-3 with it, which is their own rounding; 3% of the
-// time at 8192 x 4096 over 100352, 9% at 256 rows).
+// P in bf16 is the one rounding inside: 1.7e-3 of an entry, independent from entry to
+// entry and common to the entry's whole row of W or x.  Held in more it would be a second
+// product.  The target's entry, p - 1 from fp32, is most of a row's norm where the row
+// knows its target: what its rounding lost is kept in fp32 and added to both products
+// (333 x 1000 over 33001, rows that point at their target: 2.4e-3 of the gradients' norm
+// without it, up to 3.4e-3 for single rows, 1.66e-3 with it, the outputs' own rounding;
+// 3% of the time at 8192 x 4096 over 100352, 9% at 256 rows).  What other entries lose
+// stays: where a row points at a rival of its target as well, the gradients are 2.1e-3
+// off, single rows of dx up to 3.2e-3 and of dW up to 4.2e-3, and dW's rows of entries
+// that are no row's target 2.3e-3 with either.
 #include "head_loss.h"
 
 #include "gemm_nt.h"
