@@ -628,14 +628,13 @@ int moe_head_loss_forward(int64_t rows, int32_t cols, int32_t vocab, int32_t dty
  *   dloss   [rows] fp32: the gradient that arrives at each row's loss (1 / N for a
  *           mean over N rows)
  *   dx      [rows, cols] bf16 out;  dw [vocab, cols] bf16 out; either may be NULL
- *           (not computed), not both
- *           (rows == 0: dw alone counts, and may be NULL too)
+ *           (not computed), not both (of an empty batch, rows == 0: both too)
  *   workspace as for the forward pass
  * The vocabulary goes by in pieces, each piece's logits computed again.  P is
  * rounded to bf16 for the two products (the target's entry is held in more, so that
  * rows that know their target lose nothing by it; a row's other large entries do, up
- * to 2^-8 of each), dx and dw once more.  All sums run in a fixed order: the results are bit-reproducible.
- * rows == 0 writes zeros to dw.  Outputs must not overlap the other arguments.  The
+ * to 2^-8 of each), dx and dw once more.  All sums run in a fixed order: the results
+ * are bit-reproducible.  rows == 0 writes zeros to dw.  Outputs must not overlap the other arguments.  The
  * workspace holds nothing between calls; calls and captured graphs that may run at the
  * same time need one each. */
 int moe_head_loss_backward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,
