@@ -634,9 +634,9 @@ int moe_head_loss_forward(int64_t rows, int32_t cols, int32_t vocab, int32_t dty
  * rounded to bf16 for the two products (the target's entry is held in more, so that
  * rows that know their target lose nothing by it; a row's other large entries do, up
  * to 2^-8 of each), dx and dw once more.  All sums run in a fixed order: the results
- * are bit-reproducible.  rows == 0 writes zeros to dw.  Outputs must not overlap the other arguments.  The
- * workspace holds nothing between calls; calls and captured graphs that may run at the
- * same time need one each. */
+ * are bit-reproducible.  rows == 0 writes zeros to dw.  Outputs must not overlap the
+ * other arguments.  The workspace holds nothing between calls; calls and captured
+ * graphs that may run at the same time need one each. */
 int moe_head_loss_backward(int64_t rows, int32_t cols, int32_t vocab, int32_t dtype, const void* x, const void* w,
                            const int32_t* target, const float* lse, const float* dloss, void* dx, void* dw,
                            void* workspace, size_t workspace_bytes, void* stream);

@@ -12,6 +12,8 @@ import ctypes
 import math
 import os
 from dataclasses import dataclass
+from itertools import accumulate
+from operator import mul
 from typing import Dict, Optional
 
 import numpy as np
@@ -772,8 +774,8 @@ def _arg(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Opt
 
 
 def _flat(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Optional[int]:
-    """Address of a row-major argument (on CUDA device `device`), or None: of `shape`, flat, or
-    with its leading dimensions joined; an int allows any shape of that many elements."""
+    """Address of a row-major argument (on CUDA device `device`), or None: of `shape`, or with
+    dimensions of it joined (flat: all) or split; an int allows any shape of that many elements."""
     if t is None:
         return None
     if t.dtype is not dtype or t.get_device() != device or (t.shape != shape and not _same_order(t.shape, shape)):
@@ -785,12 +787,11 @@ def _flat(t: Optional[torch.Tensor], shape, dtype, device: int, what: str) -> Op
 
 
 def _same_order(got, shape) -> bool:
+    """Whether `got` comes from `shape` by joining neighbouring dimensions, or by splitting some."""
     if isinstance(shape, int):
         return got.numel() == shape
-    while len(got) > 1 and got[0] == 1 and got != shape:
-        got = got[1:]
-    joined = len(shape) - len(got)                     # dimensions that the first one of `got` holds beside its own
-    return joined >= 0 and len(got) > 0 and got[0] == math.prod(shape[:joined + 1]) and got[1:] == shape[joined + 1:]
+    ends, wanted = (set(accumulate(d, mul)) for d in (got, shape))     # where each one's dimensions end, in elements
+    return math.prod(got) == math.prod(shape) and (ends <= wanted or wanted <= ends)
 
 
 def _workspace_arg(t: Optional[torch.Tensor], device: int) -> Optional[int]:

@@ -6,9 +6,11 @@ from mixture_experts_transformer_moe_amd import binding as M
 
 
 @pytest.mark.parametrize("shape,good,bad", [
-    ((4, 6, 3), [(4, 6, 3), (24, 3), (72,), (1, 4, 6, 3)], [(4, 3, 6), (6, 4, 3), (4, 18), (3, 24), (4, 6, 3, 1), (2, 2, 6, 3)]),
-    ((6, 3), [(6, 3), (18,), (1, 6, 3), (1, 1, 6, 3)], [(3, 6), (6, 1, 3), (2, 3, 3), (9, 2)]),
-    ((5,), [(5,), (1, 5)], [(5, 1), (6,)]),
+    ((4, 6, 3), [(4, 6, 3), (24, 3), (72,), (1, 4, 6, 3), (2, 2, 6, 3), (4, 18), (4, 6, 3, 1)],
+     [(4, 3, 6), (6, 4, 3), (3, 24), (8, 9), (4, 6, 4)]),
+    ((6, 3), [(6, 3), (18,), (1, 6, 3), (1, 1, 6, 3), (6, 1, 3), (2, 3, 3)], [(3, 6), (9, 2), (2, 9), (6, 2)]),
+    ((5,), [(5,), (1, 5), (5, 1)], [(6,), (1, 4)]),
+    ((0, 8), [(0, 8), (0,)], [(1,), (8,)]),
     (7, [(7,), (1, 7), (7, 1)], [(8,)]),
 ])
 def test_shapes(shape, good, bad):
